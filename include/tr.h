@@ -406,6 +406,115 @@ tr_status tr_out_projection(const void *o, int64_t o_stride, const void *W_o, co
                             int32_t hv, float *x_out, void *stream);
 
 /*
+ * ------------------------------------------------ 8-bit projection steps
+ * The dense steps of a layer whose projections run in 8 bits (the pages give no precision;
+ * these stand beside the bf16 steps above).  An 8-bit operand is e4m3 values (1 byte, row-major,
+ * K contiguous) with fp32 scales, value = q * scale: an activation [T, K] has one scale per row
+ * and 128 columns, a_scale [T, ceil(K / 128)]; a weight [N, K] one per 128 x 128 tile,
+ * w_scale [ceil(N / 128), ceil(K / 128)].  The last block of a row or column may be partial.
+ * Quantisation of a block with largest magnitude m (fp32, round to nearest even):
+ *   scale = max(m / 448, 2^-126),  q = e4m3(value * (1 / scale)).
+ * A NaN in a block makes its scale and values NaN; an infinity makes its scale infinite, so
+ * that the block reads back as NaN.  Widths are multiples of 16.  No call needs a workspace;
+ * all may be captured into a graph (tr_projection_fp8 after one uncaptured call on the device).
+ *
+ * tr_rmsnorm_fp8: the RMSNorm of the sum of x and the residual stream, as an 8-bit activation.
+ *   r = x + residual (fp32; r = x without one)
+ *   n = r / sqrt(mean_j r_j^2 + eps) * gain, quantised per row and 128 columns
+ *   res_out = r rounded to the residual's type (n is computed from the unrounded r)
+ *   x         [n_rows, D] of x_dtype (bf16 or fp32), row stride x_stride elements (0 = D)
+ *   residual  [n_rows, D] of res_dtype (bf16 or fp32), or NULL
+ *   gain [D] fp32 or NULL (ones); eps 0 -> 1e-6
+ *   q [n_rows, D] e4m3, scale [n_rows, ceil(D / 128)] fp32, packed
+ *   res_out   [n_rows, D] of res_dtype, or NULL; may be the residual itself (same stride)
+ * D a multiple of 16, at most 32768; rows 16-byte aligned.
+ */
+tr_status tr_rmsnorm_fp8(const void *x, int32_t x_dtype, int64_t x_stride, const void *residual,
+                         int32_t res_dtype, int64_t res_stride, const float *gain, int64_t n_rows,
+                         int32_t d_model, float eps, uint8_t *q, float *scale, void *res_out,
+                         int64_t res_out_stride, void *stream);
+
+/* tr_quantize_fp8: x [n_rows, n_cols] of x_dtype as an 8-bit operand: block_rows = 1 for an
+ * activation, 128 for a weight.  q [n_rows, n_cols] e4m3 and
+ * scale [ceil(n_rows / block_rows), ceil(n_cols / 128)] fp32, packed.  n_cols a multiple of 16;
+ * rows of x 16-byte aligned, x_stride elements apart (0 = n_cols). */
+tr_status tr_quantize_fp8(const void *x, int32_t x_dtype, int64_t x_stride, int64_t n_rows, int32_t n_cols,
+                          int32_t block_rows, uint8_t *q, float *scale, void *stream);
+
+/* tr_projection_fp8: y = a w^T for two 8-bit operands,
+ *   y[t, n] = sum_b a_scale[t, b] w_scale[n / 128, b] sum_{k in block b} a[t, k] w[n, k],
+ * the sums in fp32 (tcgen05), y rounded once.
+ *   a [n_tokens, n_in], w [n_out, n_in] e4m3, rows 16-byte aligned and a_stride / w_stride bytes
+ *   apart (0 = n_in); y [n_tokens, n_out] of y_dtype (bf16 or fp32), rows y_stride elements
+ *   apart (0 = n_out; any alignment).  n_in a multiple of 16, n_out any. */
+tr_status tr_projection_fp8(const uint8_t *a, int64_t a_stride, const float *a_scale, const uint8_t *w,
+                            int64_t w_stride, const float *w_scale, int64_t n_tokens, int32_t n_out,
+                            int32_t n_in, void *y, int32_t y_dtype, int64_t y_stride, void *stream);
+
+/*
+ * ---------------------------------------------------- tr_linear_recurrence
+ * The gated linear recurrence with one gate per channel (the diagonal counterpart of Eq. (1):
+ * a state per channel instead of a matrix per head), over a packed batch of sequences:
+ *   h_t = a_t h_{t-1} + x_t,  y_t = h_t,  h_final = h at each sequence's last token
+ *   a_t = exp(gate_t), or with TR_GATE_LOGITS a_t = exp(-softplus(gate_t)) = 1 / (1 + e^gate_t)
+ * from h0 (NULL: zero start, as in a tail replay).  States and sums are fp32; y is rounded once.
+ * The result is bitwise reproducible, and no value of one sequence reaches another.  A batch of
+ * one token per sequence (decoding) is a call like any other: h_final may be h0, in place.
+ *   x       [T, C] of dtype, gate [T, C] of gate_dtype (bf16 or fp32 each), token strides
+ *           x_stride / gate_stride / y_stride elements (0 = C); any alignment of whole elements.
+ *           Gates are not checked: exp(gate) > 1 grows, as written.
+ *   cu_seqlens, cu_seqlens_host   as in tr_gdn_scan (empty sequences keep their state)
+ *   h0      [N, C] fp32 or NULL
+ *   y       [T, C] of dtype, or NULL to keep the final states only; not x or gate
+ *   h_final [N, C] fp32
+ * No workspace; may be captured into a graph (a replay reads cu_seqlens again, but its spread
+ * over the GPU is the captured call's: keep the same offsets).
+ */
+enum { TR_GATE_LOGITS = 512u };  /* tr_linear_recurrence(_backward): the gate is a logit */
+
+typedef struct tr_recurrence_args {
+  int32_t n_seqs, n_channels;
+  int64_t total_tokens;
+  int32_t dtype, gate_dtype;
+  uint32_t flags;
+  int64_t x_stride, gate_stride, y_stride;
+  const void *x, *gate;
+  const int32_t *cu_seqlens;
+  const int32_t *cu_seqlens_host;
+  const float *h0;
+  void *y;
+  float *h_final;
+} tr_recurrence_args;
+
+tr_status tr_linear_recurrence(const tr_recurrence_args *args, void *stream);
+
+/*
+ * Its gradients, given dy = dL/dy and (optional) dh_final = dL/dh_final:
+ *   G_t = dy_t + a_{t+1} G_{t+1}   (behind a sequence's last token: dh_final, or 0)
+ *   dx = G,  dgate_t = G_t a_t h_{t-1}  (with TR_GATE_LOGITS times -(1 - a_t)),  dh0 = a_1 G_1
+ * h_{t-1} is read from y, the forward call's output (of dtype: its rounding is the only one in
+ * front of dgate's own), and from h0 (NULL: 0) at a sequence's first token.
+ *   dy, y, dx [T, C] of dtype; gate, dgate [T, C] of gate_dtype; strides as above
+ *   h0, dh_final [N, C] fp32 or NULL;  dh0 [N, C] fp32 or NULL (may be dh_final, in place)
+ * dx and dgate must not be dy, gate, y or each other.
+ */
+typedef struct tr_recurrence_grad_args {
+  int32_t n_seqs, n_channels;
+  int64_t total_tokens;
+  int32_t dtype, gate_dtype;
+  uint32_t flags;
+  int64_t dy_stride, gate_stride, y_stride, dx_stride, dgate_stride;
+  const void *dy, *gate, *y;
+  const int32_t *cu_seqlens;
+  const int32_t *cu_seqlens_host;
+  const float *h0, *dh_final;
+  void *dx, *dgate;
+  float *dh0;
+} tr_recurrence_grad_args;
+
+tr_status tr_linear_recurrence_backward(const tr_recurrence_grad_args *args, void *stream);
+
+/*
  * tr_set_wait_limit_ns: the wall-clock limit of every bounded wait in the chunked scan's
  * kernels (their mbarrier waits on copies, products and the other roles of a CTA), for
  * calls made after it; 0 restores the default of 4 s, above 60 s is rejected.  A wait that

@@ -24,6 +24,7 @@ TR_DTYPE_F32, TR_DTYPE_BF16 = 0, 1
 TR_NORMALIZE_QK, TR_SKIP_LAST_OUTPUT, TR_SCAN_RECURRENT, TR_SKIP_LAST_FFN = 1, 2, 4, 8
 TR_OUTPUT_GATE = 16
 TR_SCAN_STALL_TEST = 256
+TR_GATE_LOGITS = 512
 
 STATUS_NAMES = {0: "TR_OK", 1: "TR_ERR_INVALID_ARG", 2: "TR_ERR_SHAPE", 3: "TR_ERR_DTYPE",
                 4: "TR_ERR_ALIGNMENT", 5: "TR_ERR_UNSUPPORTED", 6: "TR_ERR_WORKSPACE",
@@ -57,6 +58,23 @@ class GroupArgs(ctypes.Structure):
                 ("conv_width", c_i32), ("conv_state", c_vp)]
 
 
+class RecurrenceArgs(ctypes.Structure):
+    _fields_ = [("n_seqs", c_i32), ("n_channels", c_i32), ("total_tokens", c_i64),
+                ("dtype", c_i32), ("gate_dtype", c_i32), ("flags", c_u32), ("x_stride", c_i64),
+                ("gate_stride", c_i64), ("y_stride", c_i64), ("x", c_vp), ("gate", c_vp),
+                ("cu_seqlens", c_vp), ("cu_seqlens_host", c_vp), ("h0", c_vp), ("y", c_vp),
+                ("h_final", c_vp)]
+
+
+class RecurrenceGradArgs(ctypes.Structure):
+    _fields_ = [("n_seqs", c_i32), ("n_channels", c_i32), ("total_tokens", c_i64),
+                ("dtype", c_i32), ("gate_dtype", c_i32), ("flags", c_u32), ("dy_stride", c_i64),
+                ("gate_stride", c_i64), ("y_stride", c_i64), ("dx_stride", c_i64),
+                ("dgate_stride", c_i64), ("dy", c_vp), ("gate", c_vp), ("y", c_vp),
+                ("cu_seqlens", c_vp), ("cu_seqlens_host", c_vp), ("h0", c_vp),
+                ("dh_final", c_vp), ("dx", c_vp), ("dgate", c_vp), ("dh0", c_vp)]
+
+
 # exported symbol -> (restype, argtypes)
 _SIGNATURES = {
     "tr_last_error": (ctypes.c_char_p, []),
@@ -86,6 +104,13 @@ _SIGNATURES = {
                                         c_f32, c_vp, c_vp, c_vp, c_vp]),
     "tr_out_projection": (ctypes.c_int, [c_vp, c_i64, c_vp, c_vp, c_i32, c_i64, c_i32, c_i32,
                                          c_vp, c_vp]),
+    "tr_rmsnorm_fp8": (ctypes.c_int, [c_vp, c_i32, c_i64, c_vp, c_i32, c_i64, c_vp, c_i64, c_i32,
+                                      c_f32, c_vp, c_vp, c_vp, c_i64, c_vp]),
+    "tr_quantize_fp8": (ctypes.c_int, [c_vp, c_i32, c_i64, c_i64, c_i32, c_i32, c_vp, c_vp, c_vp]),
+    "tr_projection_fp8": (ctypes.c_int, [c_vp, c_i64, c_vp, c_vp, c_i64, c_vp, c_i64, c_i32, c_i32,
+                                         c_vp, c_i32, c_i64, c_vp]),
+    "tr_linear_recurrence": (ctypes.c_int, [ctypes.POINTER(RecurrenceArgs), c_vp]),
+    "tr_linear_recurrence_backward": (ctypes.c_int, [ctypes.POINTER(RecurrenceGradArgs), c_vp]),
     "tr_check": (ctypes.c_int, [c_vp]),
     "tr_set_wait_limit_ns": (ctypes.c_int, [ctypes.c_uint64]),
 }
@@ -555,6 +580,207 @@ def out_projection(o, W_o, x_res, stream=None):
                                   _ptr(x_res), _dtype_code(x_res), T, D, hv, _ptr(out),
                                   _stream(stream, dev)), "tr_out_projection")
     return out
+
+
+# ------------------------------------------------------------ 8-bit projection steps, recurrence
+
+_FP8 = torch.float8_e4m3fn
+_DTYPES = {torch.float32: TR_DTYPE_F32, torch.bfloat16: TR_DTYPE_BF16}
+
+
+def _enqueue(dev, stream, call):
+    """call(raw stream handle) with the tensors' device current, on its current stream or on
+    `stream`; what `call` allocates then belongs to the stream that its kernels run on."""
+    if stream is None:
+        if torch.cuda.current_device() == dev.index:
+            return call(torch.cuda.current_stream().cuda_stream)
+        with torch.cuda.device(dev):
+            return call(torch.cuda.current_stream().cuda_stream)
+    if getattr(stream, "device", dev) != dev:
+        raise ValueError("the stream belongs to %s, the tensors to %s" % (stream.device, dev))
+    with torch.cuda.stream(stream):
+        return call(stream.cuda_stream)
+
+
+def _row_stride(name, t, shape, dtypes):
+    """The row stride of a [rows, columns] operand of one of `dtypes` whose rows are contiguous
+    and apart (0, packed, for a single row)."""
+    if t.dtype not in dtypes:
+        raise TypeError("%s: unsupported dtype %s" % (name, t.dtype))
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    if shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError("%s must have contiguous rows" % name)
+    if shape[0] <= 1:
+        return 0
+    if t.stride(0) < shape[1]:
+        raise ValueError("%s has overlapping rows (stride %d)" % (name, t.stride(0)))
+    return t.stride(0)
+
+
+def _matrix(name, t):
+    if t.dim() != 2:
+        raise ValueError("%s must be a matrix, got %d dimensions" % (name, t.dim()))
+    return t.shape
+
+
+def _blocks128(n):
+    return (n + 127) // 128
+
+
+def rmsnorm_fp8(x, gain=None, eps=0.0, *, residual=None, q=None, scale=None, residual_out=None,
+                stream=None):
+    """RMSNorm of x (+ residual) as an 8-bit activation: (q [T, D] e4m3, scale [T, ceil(D/128)]
+    fp32, residual_out = x + residual in the residual's type, or None without a residual).
+    residual_out may be the residual itself."""
+    T, D = _matrix("x", x)
+    dev = _need_cuda(x, gain, residual, q, scale, residual_out)
+    xs = _row_stride("x", x, (T, D), _DTYPES)
+    _need_layout("gain", gain, torch.float32, (D,))
+    _need_layout("q", q, _FP8, (T, D))
+    _need_layout("scale", scale, torch.float32, (T, _blocks128(D)))
+    rs = ro = rd = 0
+    if residual is not None:
+        rs = _row_stride("residual", residual, (T, D), _DTYPES)
+        rd = _DTYPES[residual.dtype]
+        if residual_out is not None:
+            ro = _row_stride("residual_out", residual_out, (T, D), (residual.dtype,))
+    elif residual_out is not None:
+        raise ValueError("residual_out without a residual")
+
+    def call(handle):
+        qq = q if q is not None else torch.empty((T, D), dtype=_FP8, device=dev)
+        sc = scale if scale is not None else torch.empty((T, _blocks128(D)), dtype=torch.float32,
+                                                         device=dev)
+        out = residual_out
+        if residual is not None and out is None:
+            out = torch.empty((T, D), dtype=residual.dtype, device=dev)
+        _ok(lib.tr_rmsnorm_fp8(x.data_ptr(), _DTYPES[x.dtype], xs, _ptr(residual), rd, rs,
+                               _ptr(gain), T, D, float(eps), qq.data_ptr(), sc.data_ptr(),
+                               _ptr(out), ro, handle), "tr_rmsnorm_fp8")
+        return qq, sc, out
+    return _enqueue(dev, stream, call)
+
+
+def quantize_fp8(x, *, block_rows=1, q=None, scale=None, stream=None):
+    """x [R, C] as an 8-bit operand: (q [R, C] e4m3, scale [ceil(R/block_rows), ceil(C/128)]
+    fp32); block_rows 1 for an activation, 128 for a weight."""
+    R, C = _matrix("x", x)
+    dev = _need_cuda(x, q, scale)
+    xs = _row_stride("x", x, (R, C), _DTYPES)
+    if block_rows not in (1, 128):
+        raise ValueError("block_rows must be 1 or 128")
+    sshape = ((R + block_rows - 1) // block_rows, _blocks128(C))
+    _need_layout("q", q, _FP8, (R, C))
+    _need_layout("scale", scale, torch.float32, sshape)
+
+    def call(handle):
+        qq = q if q is not None else torch.empty((R, C), dtype=_FP8, device=dev)
+        sc = scale if scale is not None else torch.empty(sshape, dtype=torch.float32, device=dev)
+        _ok(lib.tr_quantize_fp8(x.data_ptr(), _DTYPES[x.dtype], xs, R, C, block_rows, qq.data_ptr(),
+                                sc.data_ptr(), handle), "tr_quantize_fp8")
+        return qq, sc
+    return _enqueue(dev, stream, call)
+
+
+def projection_fp8(a, a_scale, w, w_scale, *, out_dtype=torch.bfloat16, y=None, stream=None):
+    """y = a w^T [T, N] for an 8-bit activation a [T, K] and weight w [N, K] (e4m3 with the
+    scales of quantize_fp8 / rmsnorm_fp8), fp32 sums, in out_dtype (bf16 or fp32; y's if given)."""
+    T, K = _matrix("a", a)
+    N = _matrix("w", w)[0]
+    dev = _need_cuda(a, a_scale, w, w_scale, y)
+    as_ = _row_stride("a", a, (T, K), (_FP8,))
+    ws = _row_stride("w", w, (N, K), (_FP8,))
+    _need_layout("a_scale", a_scale, torch.float32, (T, _blocks128(K)))
+    _need_layout("w_scale", w_scale, torch.float32, (_blocks128(N), _blocks128(K)))
+    ys = 0
+    if y is not None:
+        out_dtype = y.dtype
+        ys = _row_stride("y", y, (T, N), _DTYPES)
+    elif out_dtype not in _DTYPES:
+        raise TypeError("unsupported dtype %s" % out_dtype)
+
+    def call(handle):
+        out = y if y is not None else torch.empty((T, N), dtype=out_dtype, device=dev)
+        _ok(lib.tr_projection_fp8(a.data_ptr(), as_, a_scale.data_ptr(), w.data_ptr(), ws,
+                                  w_scale.data_ptr(), T, N, K, out.data_ptr(), _DTYPES[out_dtype],
+                                  ys, handle), "tr_projection_fp8")
+        return out
+    return _enqueue(dev, stream, call)
+
+
+def _offsets(cu_seqlens, device):
+    """seqlens() that also refuses a pair the library would read wrongly."""
+    host, dev = _seqlens(cu_seqlens, device)
+    if host.dim() != 1 or dev.shape != host.shape or host.numel() < 1 or \
+            not host.is_contiguous() or not dev.is_contiguous():
+        raise ValueError("cu_seqlens must be N + 1 contiguous offsets")
+    return host, dev
+
+
+def linear_recurrence(x, gate, cu_seqlens, *, h0=None, gate_logits=False, want_y=True, y=None,
+                      h_final=None, stream=None):
+    """h_t = a_t h_{t-1} + x_t per channel over packed sequences: (y [T, C] or None, h_final
+    [N, C] fp32).  a = exp(gate), or exp(-softplus(gate)) with gate_logits.  h0 [N, C] fp32
+    (None: zero start); h_final may be h0.  For a captured call give cu_seqlens as seqlens()."""
+    T, C = _matrix("x", x)
+    dev = _need_cuda(x, gate, h0, y, h_final)
+    xs = _row_stride("x", x, (T, C), _DTYPES)
+    gs = _row_stride("gate", gate, (T, C), _DTYPES)
+    ys = _row_stride("y", y, (T, C), (x.dtype,)) if y is not None else 0
+
+    def call(handle):
+        host, cu = _offsets(cu_seqlens, dev)
+        N = host.numel() - 1
+        _need_layout("h0", h0, torch.float32, (N, C))
+        _need_layout("h_final", h_final, torch.float32, (N, C))
+        out = (y if y is not None else torch.empty((T, C), dtype=x.dtype, device=dev)) \
+            if want_y else None
+        fin = h_final if h_final is not None else torch.empty((N, C), dtype=torch.float32, device=dev)
+        a = RecurrenceArgs(N, C, T, _DTYPES[x.dtype], _DTYPES[gate.dtype],
+                           TR_GATE_LOGITS if gate_logits else 0, xs, gs, ys, x.data_ptr(),
+                           gate.data_ptr(), cu.data_ptr(), host.data_ptr(), _ptr(h0), _ptr(out),
+                           fin.data_ptr())
+        _ok(lib.tr_linear_recurrence(ctypes.byref(a), handle), "tr_linear_recurrence")
+        return out, fin
+    return _enqueue(dev, stream, call)
+
+
+def linear_recurrence_backward(dy, gate, y, cu_seqlens, *, h0=None, dh_final=None,
+                               gate_logits=False, want_dh0=None, dx=None, dgate=None, dh0=None,
+                               stream=None):
+    """Gradients of linear_recurrence given dy and dh_final [N, C] fp32 (None: 0): (dx [T, C],
+    dgate [T, C], dh0 [N, C] fp32 or None).  y is the forward call's output; dh0 is computed
+    where want_dh0 (by default: where there is an h0 or a dh0 to fill) and may be dh_final."""
+    T, C = _matrix("dy", dy)
+    dev = _need_cuda(dy, gate, y, h0, dh_final, dx, dgate, dh0)
+    ds = _row_stride("dy", dy, (T, C), _DTYPES)
+    gs = _row_stride("gate", gate, (T, C), _DTYPES)
+    ys = _row_stride("y", y, (T, C), (dy.dtype,))
+    dxs = _row_stride("dx", dx, (T, C), (dy.dtype,)) if dx is not None else 0
+    dgs = _row_stride("dgate", dgate, (T, C), (gate.dtype,)) if dgate is not None else 0
+    if want_dh0 is None:
+        want_dh0 = h0 is not None or dh0 is not None
+
+    def call(handle):
+        host, cu = _offsets(cu_seqlens, dev)
+        N = host.numel() - 1
+        for name, t in (("h0", h0), ("dh_final", dh_final), ("dh0", dh0)):
+            _need_layout(name, t, torch.float32, (N, C))
+        ox = dx if dx is not None else torch.empty((T, C), dtype=dy.dtype, device=dev)
+        og = dgate if dgate is not None else torch.empty((T, C), dtype=gate.dtype, device=dev)
+        oh = None
+        if want_dh0:
+            oh = dh0 if dh0 is not None else torch.empty((N, C), dtype=torch.float32, device=dev)
+        a = RecurrenceGradArgs(N, C, T, _DTYPES[dy.dtype], _DTYPES[gate.dtype],
+                               TR_GATE_LOGITS if gate_logits else 0, ds, gs, ys, dxs, dgs,
+                               dy.data_ptr(), gate.data_ptr(), y.data_ptr(), cu.data_ptr(),
+                               host.data_ptr(), _ptr(h0), _ptr(dh_final), ox.data_ptr(),
+                               og.data_ptr(), _ptr(oh))
+        _ok(lib.tr_linear_recurrence_backward(ctypes.byref(a), handle),
+            "tr_linear_recurrence_backward")
+        return ox, og, oh
+    return _enqueue(dev, stream, call)
 
 
 def set_wait_limit_ns(ns: int) -> None:

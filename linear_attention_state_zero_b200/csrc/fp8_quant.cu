@@ -1,0 +1,282 @@
+// fp8_quant.cu -- the e4m3 operands of the 8-bit projections: RMSNorm (with the residual's
+// addition) written as e4m3 with scales, and the plain quantisation of a matrix.
+//
+//   r = x + residual,  n = r / sqrt(mean r^2 + eps) * gain          (fp32; or n = x)
+//   per block of 128 columns (and block_rows rows):
+//     s = max(max|n| / 448, 2^-126),  q = e4m3(n * (1 / s))         (round to nearest even)
+//
+// 448 is e4m3's largest value; the floor of 2^-126 keeps 1 / s finite for an all-zero block
+// (its q is 0 with any scale).  A NaN in a block makes the block's scale and values NaN; an
+// infinity makes the scale infinite, so the block reads back as NaN.  The division and the
+// reciprocal are IEEE, one per block; the products round once.  r is kept in fp32 (the
+// residual output rounds it on its own), and the e4m3 rounding is the only other one.
+// HBM-bound: each input is read once into registers and each output written once.
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+
+#include "layer_ops.h"
+#include "tr_internal.h"
+#include "tr_ptx.cuh"
+
+namespace tr {
+namespace {
+
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+template <bool BF16>
+__device__ __forceinline__ void load8(const void *p, int64_t off, float (&f)[8]) {
+  if (BF16) {
+    const uint4 u = *reinterpret_cast<const uint4 *>(reinterpret_cast<const __nv_bfloat16 *>(p) + off);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = __uint_as_float(w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  } else {
+    const float4 *q = reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(p) + off);
+    const float4 a = q[0], b = q[1];
+    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+  }
+}
+
+template <bool BF16>
+__device__ __forceinline__ void store8(void *p, int64_t off, const float (&f)[8]) {
+  if (BF16) {
+    *reinterpret_cast<uint4 *>(reinterpret_cast<__nv_bfloat16 *>(p) + off) =
+        make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                   pack_bf16x2(f[6], f[7]));
+  } else {
+    float4 *q = reinterpret_cast<float4 *>(reinterpret_cast<float *>(p) + off);
+    q[0] = make_float4(f[0], f[1], f[2], f[3]);
+    q[1] = make_float4(f[4], f[5], f[6], f[7]);
+  }
+}
+
+__device__ __forceinline__ float abs_max8(const float (&f)[8]) {
+  float m = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max_nan(m, fabsf(f[i]));
+  return m;
+}
+
+// The scale of a block whose largest magnitude is m.
+__device__ __forceinline__ float scale_of(float m) {
+  return max_nan(__fdiv_rn(m, 448.f), 1.17549435e-38f);
+}
+
+__device__ __forceinline__ void store_q8(uint8_t *dst, const float (&f)[8], float inv) {
+  uint32_t w[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(f[4 * h] * inv, f[4 * h + 1] * inv),
+                                                 __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(f[4 * h + 2] * inv, f[4 * h + 3] * inv),
+                                                 __NV_SATFINITE, __NV_E4M3);
+    w[h] = lo | (hi << 16);
+  }
+  *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
+}
+
+constexpr int kNV = 4;   // 8-element vectors a lane holds of its row
+
+// WPR warps share a row (at most WPR * 1024 columns): vector v of the row is lane v % 32 of
+// warp (v / 32) % WPR, so 16 neighbouring lanes hold a scale block and each warp's accesses
+// are contiguous.  A few vectors per lane and several warps per row, rather than a warp per
+// row with the whole row in its registers, so that a few rows use many warps too.
+template <bool XBF, bool RES, bool RBF, int WPR>
+__global__ void __launch_bounds__(WPR < 8 ? 256 : WPR * 32)
+    rmsnorm_fp8_kernel(NormFp8Launch p) {
+  constexpr int kRows = WPR < 8 ? 8 / WPR : 1;   // rows of a block
+  __shared__ float part[kRows][WPR];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int wr = warp % WPR, slot = warp / WPR;
+  const int64_t row = (int64_t)blockIdx.x * kRows + slot;
+  const bool live = row < p.rows;
+  pdl_trigger();
+  pdl_wait();
+  float f[kNV][8];
+  float ss = 0.f;
+#pragma unroll
+  for (int j = 0; j < kNV; ++j) {
+    const int c = ((j * WPR + wr) * 32 + lane) * 8;
+    const bool in = live && c < p.D;
+    if (in) load8<XBF>(p.x, row * p.x_stride + c, f[j]);
+    else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[j][i] = 0.f;
+    }
+    if (RES && in) {
+      float r[8];
+      load8<RBF>(p.res, row * p.res_stride + c, r);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[j][i] += r[i];
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < kNV; ++j) {
+    const int c = ((j * WPR + wr) * 32 + lane) * 8;
+    if (RES && p.res_out && live && c < p.D)
+      store8<RBF>(p.res_out, row * p.res_out_stride + c, f[j]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ss = fmaf(f[j][i], f[j][i], ss);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+  if (WPR > 1) {
+    if (lane == 0) part[slot][wr] = ss;
+    __syncthreads();
+    ss = 0.f;
+#pragma unroll
+    for (int w = 0; w < WPR; ++w) ss += part[slot][w];
+  }
+  const float rms = rsqrtf(ss / (float)p.D + p.eps);
+  const int kb = (p.D + kScaleBlock - 1) / kScaleBlock;
+#pragma unroll
+  for (int j = 0; j < kNV; ++j) {
+    const int c = ((j * WPR + wr) * 32 + lane) * 8;
+    const bool in = live && c < p.D;
+    float g[8];
+    if (p.gain && in) load8<false>(p.gain, c, g);
+    else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) g[i] = 1.f;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[j][i] = f[j][i] * rms * g[i];
+    float m = abs_max8(f[j]);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float s = scale_of(m);
+    if (in) {
+      store_q8(p.q + row * p.D + c, f[j], __frcp_rn(s));
+      if ((lane & 15) == 0) p.scale[row * kb + c / kScaleBlock] = s;
+    }
+  }
+}
+
+// One scale per row and 128 columns: a warp takes units of 256 columns of a row, kNV of them
+// at a time with all their loads in flight.
+template <bool XBF>
+__global__ void __launch_bounds__(256) quantize_rows_kernel(QuantFp8Launch p) {
+  const int lane = threadIdx.x & 31;
+  const int upr = (p.cols + 255) / 256;   // units per row
+  const int kb = (p.cols + kScaleBlock - 1) / kScaleBlock;
+  const int64_t units = p.rows * upr;
+  const int64_t u0 = ((int64_t)blockIdx.x * 8 + (threadIdx.x >> 5)) * kNV;
+  pdl_trigger();
+  pdl_wait();
+  float f[kNV][8];
+#pragma unroll
+  for (int j = 0; j < kNV; ++j) {
+    const int64_t u = u0 + j, row = u / upr;
+    const int c = (int)(u - row * upr) * 256 + lane * 8;
+    if (u < units && c < p.cols) load8<XBF>(p.x, row * p.x_stride + c, f[j]);
+    else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[j][i] = 0.f;
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < kNV; ++j) {
+    const int64_t u = u0 + j, row = u / upr;
+    const int c = (int)(u - row * upr) * 256 + lane * 8;
+    float m = abs_max8(f[j]);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float s = scale_of(m);
+    if (u < units && c < p.cols) {
+      store_q8(p.q + row * p.cols + c, f[j], __frcp_rn(s));
+      if ((lane & 15) == 0) p.scale[row * kb + c / kScaleBlock] = s;
+    }
+  }
+}
+
+// One scale per 128 x 128 tile: a block holds the tile in registers, 8 rows per thread
+// (16 lanes across the columns, 16 row groups).
+template <bool XBF>
+__global__ void __launch_bounds__(256) quantize_tile_kernel(QuantFp8Launch p) {
+  __shared__ float part[8];
+  const int kb = (p.cols + kScaleBlock - 1) / kScaleBlock;
+  const int64_t rb = blockIdx.x / kb;
+  const int cb = (int)(blockIdx.x - rb * kb);
+  const int c = cb * kScaleBlock + (threadIdx.x & 15) * 8;
+  const int64_t r0 = rb * kScaleBlock + (threadIdx.x >> 4);
+  pdl_trigger();
+  pdl_wait();
+  float f[8][8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    if (r0 + 16 * j < p.rows && c < p.cols) load8<XBF>(p.x, (r0 + 16 * j) * p.x_stride + c, f[j]);
+    else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[j][i] = 0.f;
+    }
+  }
+  float m = 0.f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) m = max_nan(m, abs_max8(f[j]));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < 8; ++w) m = max_nan(m, part[w]);
+  const float s = scale_of(m);
+  const float inv = __frcp_rn(s);
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (r0 + 16 * j < p.rows && c < p.cols) store_q8(p.q + (r0 + 16 * j) * p.cols + c, f[j], inv);
+  if (threadIdx.x == 0) p.scale[rb * kb + cb] = s;
+}
+
+template <bool XBF, bool RES, bool RBF>
+cudaError_t launch_norm(const NormFp8Launch &p, cudaStream_t s, bool pdl) {
+  auto go = [&](auto kern, int wpr) {
+    const int rows = wpr < 8 ? 8 / wpr : 1;
+    return launch_kernel(kern, dim3((unsigned)((p.rows + rows - 1) / rows)),
+                         dim3(wpr < 8 ? 256 : wpr * 32), 0, s, pdl, p);
+  };
+  // the fewest warps that hold the row (1024 columns each)
+  if (p.D <= 1024) return go(rmsnorm_fp8_kernel<XBF, RES, RBF, 1>, 1);
+  if (p.D <= 2048) return go(rmsnorm_fp8_kernel<XBF, RES, RBF, 2>, 2);
+  if (p.D <= 4096) return go(rmsnorm_fp8_kernel<XBF, RES, RBF, 4>, 4);
+  if (p.D <= 8192) return go(rmsnorm_fp8_kernel<XBF, RES, RBF, 8>, 8);
+  if (p.D <= 16384) return go(rmsnorm_fp8_kernel<XBF, RES, RBF, 16>, 16);
+  return go(rmsnorm_fp8_kernel<XBF, RES, RBF, 32>, 32);
+}
+
+}  // namespace
+
+cudaError_t launch_rmsnorm_fp8(const NormFp8Launch &p, cudaStream_t s, bool pdl) {
+  if (p.rows <= 0) return cudaSuccess;
+  if (!p.res)
+    return p.x_bf16 ? launch_norm<true, false, false>(p, s, pdl)
+                    : launch_norm<false, false, false>(p, s, pdl);
+  if (p.res_bf16)
+    return p.x_bf16 ? launch_norm<true, true, true>(p, s, pdl)
+                    : launch_norm<false, true, true>(p, s, pdl);
+  return p.x_bf16 ? launch_norm<true, true, false>(p, s, pdl)
+                  : launch_norm<false, true, false>(p, s, pdl);
+}
+
+cudaError_t launch_quantize_fp8(const QuantFp8Launch &p, cudaStream_t s, bool pdl) {
+  if (p.rows <= 0) return cudaSuccess;
+  if (p.block_rows == kScaleBlock) {
+    const int64_t tiles = ((p.rows + kScaleBlock - 1) / kScaleBlock) *
+                          ((p.cols + kScaleBlock - 1) / kScaleBlock);
+    return p.x_bf16 ? launch_kernel(quantize_tile_kernel<true>, dim3((unsigned)tiles), dim3(256), 0, s, pdl, p)
+                    : launch_kernel(quantize_tile_kernel<false>, dim3((unsigned)tiles), dim3(256), 0, s, pdl, p);
+  }
+  const int64_t units = p.rows * ((p.cols + 255) / 256);
+  const int64_t blocks = (units + 8 * kNV - 1) / (8 * kNV);
+  return p.x_bf16 ? launch_kernel(quantize_rows_kernel<true>, dim3((unsigned)blocks), dim3(256), 0, s, pdl, p)
+                  : launch_kernel(quantize_rows_kernel<false>, dim3((unsigned)blocks), dim3(256), 0, s, pdl, p);
+}
+
+}  // namespace tr

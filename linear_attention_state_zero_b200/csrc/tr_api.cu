@@ -15,6 +15,7 @@
 #include <vector>
 
 #include "../../include/tr.h"
+#include "layer_ops.h"
 #include "tr_internal.h"
 
 namespace {
@@ -1101,6 +1102,243 @@ tr_status tr_out_projection(const void *o, int64_t o_stride, const void *W_o, co
                                         static_cast<cudaStream_t>(stream), true, &err);
   if (e != cudaSuccess)
     return err.empty() ? cuda_fail(e, "output projection") : fail(TR_ERR_CUDA, "%s", err.c_str());
+  return ok();
+}
+
+// ------------------------------------------------- 8-bit projection steps
+namespace {
+
+// rows x cols of e4m3 output: whole 16-byte pieces per row, and a grid that fits
+tr_status check_fp8_shape(int64_t rows, int64_t cols, const char *what) {
+  if (rows < 0 || cols <= 0) return fail(TR_ERR_INVALID_ARG, "%s: bad sizes", what);
+  if (cols % 16) return fail(TR_ERR_UNSUPPORTED, "%s: %lld columns are not a multiple of 16", what, (long long)cols);
+  if (rows > 0x7fffffffLL || cols > (1 << 20) || rows > (1LL << 40) / cols)
+    return fail(TR_ERR_UNSUPPORTED, "%s: %lld x %lld is too large", what, (long long)rows, (long long)cols);
+  return TR_OK;
+}
+
+// a row stride (0: packed) of elements of `esz` bytes, every row 16-byte aligned
+tr_status check_stride(int64_t *stride, int64_t cols, int esz, const char *what) {
+  if (*stride == 0) *stride = cols;
+  if (*stride < cols) return fail(TR_ERR_SHAPE, "%s: the row stride is smaller than the row", what);
+  if ((*stride * esz) % 16) return fail(TR_ERR_ALIGNMENT, "%s: rows must be 16-byte aligned", what);
+  return TR_OK;
+}
+
+bool known_dtype(int32_t d) { return d == TR_DTYPE_F32 || d == TR_DTYPE_BF16; }
+int dtype_size(int32_t d) { return d == TR_DTYPE_BF16 ? 2 : 4; }
+bool aligned_to(const void *p, int n) { return (reinterpret_cast<uintptr_t>(p) % (uintptr_t)n) == 0; }
+
+}  // namespace
+
+tr_status tr_rmsnorm_fp8(const void *x, int32_t x_dtype, int64_t x_stride, const void *residual,
+                         int32_t res_dtype, int64_t res_stride, const float *gain, int64_t n_rows,
+                         int32_t d_model, float eps, uint8_t *q, float *scale, void *res_out,
+                         int64_t res_out_stride, void *stream) {
+  tr_status st = check_fp8_shape(n_rows, d_model, "rmsnorm_fp8");
+  if (st != TR_OK) return st;
+  if (d_model > 32768) return fail(TR_ERR_UNSUPPORTED, "d_model = %d (at most 32768)", d_model);
+  if (!known_dtype(x_dtype) || (residual && !known_dtype(res_dtype))) return fail(TR_ERR_DTYPE, "x_dtype/res_dtype");
+  if (n_rows > 0 && (!x || !q || !scale)) return fail(TR_ERR_INVALID_ARG, "a required pointer is NULL");
+  if (res_out && !residual) return fail(TR_ERR_INVALID_ARG, "res_out without a residual");
+  if (!aligned16(x) || !aligned16(q) || !aligned4(scale) || !aligned16(residual) || !aligned16(res_out) ||
+      !aligned16(gain))
+    return fail(TR_ERR_ALIGNMENT, "x/residual/gain/q/res_out must be 16-byte aligned");
+  if ((st = check_stride(&x_stride, d_model, dtype_size(x_dtype), "x")) != TR_OK) return st;
+  if (residual && ((st = check_stride(&res_stride, d_model, dtype_size(res_dtype), "residual")) != TR_OK ||
+                   (st = check_stride(&res_out_stride, d_model, dtype_size(res_dtype), "res_out")) != TR_OK))
+    return st;
+  tr::NormFp8Launch p{};
+  p.x = x;
+  p.x_bf16 = x_dtype == TR_DTYPE_BF16;
+  p.x_stride = x_stride;
+  p.res = residual;
+  p.res_bf16 = residual && res_dtype == TR_DTYPE_BF16;
+  p.res_stride = res_stride;
+  p.res_out = res_out;
+  p.res_out_stride = res_out_stride;
+  p.gain = gain;
+  p.rows = n_rows;
+  p.D = d_model;
+  p.eps = eps > 0.f ? eps : 1e-6f;
+  p.q = q;
+  p.scale = scale;
+  cudaError_t e = tr::launch_rmsnorm_fp8(p, static_cast<cudaStream_t>(stream), true);
+  if (e != cudaSuccess) return cuda_fail(e, "rmsnorm_fp8");
+  return ok();
+}
+
+tr_status tr_quantize_fp8(const void *x, int32_t x_dtype, int64_t x_stride, int64_t n_rows, int32_t n_cols,
+                          int32_t block_rows, uint8_t *q, float *scale, void *stream) {
+  tr_status st = check_fp8_shape(n_rows, n_cols, "quantize_fp8");
+  if (st != TR_OK) return st;
+  if (!known_dtype(x_dtype)) return fail(TR_ERR_DTYPE, "x_dtype");
+  if (block_rows != 1 && block_rows != 128)
+    return fail(TR_ERR_UNSUPPORTED, "block_rows = %d (1 or 128)", block_rows);
+  if (n_rows > 0 && (!x || !q || !scale)) return fail(TR_ERR_INVALID_ARG, "a required pointer is NULL");
+  if (!aligned16(x) || !aligned16(q) || !aligned4(scale))
+    return fail(TR_ERR_ALIGNMENT, "x/q must be 16-byte aligned");
+  if ((st = check_stride(&x_stride, n_cols, dtype_size(x_dtype), "x")) != TR_OK) return st;
+  tr::QuantFp8Launch p{};
+  p.x = x;
+  p.x_bf16 = x_dtype == TR_DTYPE_BF16;
+  p.x_stride = x_stride;
+  p.rows = n_rows;
+  p.cols = n_cols;
+  p.block_rows = block_rows;
+  p.q = q;
+  p.scale = scale;
+  cudaError_t e = tr::launch_quantize_fp8(p, static_cast<cudaStream_t>(stream), true);
+  if (e != cudaSuccess) return cuda_fail(e, "quantize_fp8");
+  return ok();
+}
+
+tr_status tr_projection_fp8(const uint8_t *a, int64_t a_stride, const float *a_scale, const uint8_t *w,
+                            int64_t w_stride, const float *w_scale, int64_t n_tokens, int32_t n_out,
+                            int32_t n_in, void *y, int32_t y_dtype, int64_t y_stride, void *stream) {
+  if (n_tokens < 0 || n_tokens > 0x7fffffffLL || n_out <= 0 || n_in <= 0)
+    return fail(TR_ERR_INVALID_ARG, "bad sizes");
+  if (n_in % 16) return fail(TR_ERR_UNSUPPORTED, "n_in = %d is not a multiple of 16", n_in);
+  if (((n_tokens + 127) / 128) * (((int64_t)n_out + 127) / 128) > 0x7fffffffLL)
+    return fail(TR_ERR_UNSUPPORTED, "%lld x %d outputs are too many", (long long)n_tokens, n_out);
+  if (!known_dtype(y_dtype)) return fail(TR_ERR_DTYPE, "y_dtype");
+  if (n_tokens > 0 && (!a || !a_scale || !w || !w_scale || !y))
+    return fail(TR_ERR_INVALID_ARG, "a required pointer is NULL");
+  if (!aligned16(a) || !aligned16(w) || !aligned4(a_scale) || !aligned4(w_scale) ||
+      !aligned_to(y, dtype_size(y_dtype)))
+    return fail(TR_ERR_ALIGNMENT, "a/w must be 16-byte aligned, the scales and y to their elements");
+  tr_status st;
+  if ((st = check_stride(&a_stride, n_in, 1, "a")) != TR_OK || (st = check_stride(&w_stride, n_in, 1, "w")) != TR_OK)
+    return st;
+  if (y_stride == 0) y_stride = n_out;
+  if (y_stride < n_out) return fail(TR_ERR_SHAPE, "y: the row stride is smaller than the row");
+  if (n_tokens == 0) return ok();
+  int dev;
+  unsigned *errw;
+  std::string err;
+  if (!device_state(static_cast<cudaStream_t>(stream), &dev, &errw, &err)) return fail(TR_ERR_CUDA, "%s", err.c_str());
+  tr::GemmFp8Launch p{};
+  p.a = a;
+  p.a_stride = a_stride;
+  p.sa = a_scale;
+  p.w = w;
+  p.w_stride = w_stride;
+  p.sw = w_scale;
+  p.T = (int)n_tokens;
+  p.N = n_out;
+  p.K = n_in;
+  p.y = y;
+  p.y_bf16 = y_dtype == TR_DTYPE_BF16;
+  p.y_stride = y_stride;
+  cudaError_t e = tr::launch_gemm_fp8(p, errw, static_cast<cudaStream_t>(stream), true, &err);
+  if (e != cudaSuccess)
+    return err.empty() ? cuda_fail(e, "projection_fp8") : fail(TR_ERR_CUDA, "%s", err.c_str());
+  return ok();
+}
+
+// --------------------------------------------------- gated linear recurrence
+namespace {
+
+tr_status check_recurrence(int32_t n_seqs, int32_t C, int64_t T, int32_t dtype, int32_t gate_dtype,
+                           uint32_t flags, const int32_t *cu, const int32_t *cu_host) {
+  if (n_seqs < 0 || C <= 0 || T < 0) return fail(TR_ERR_INVALID_ARG, "negative or zero size");
+  if (T > 0x7fff0000LL || C > (1 << 24))
+    return fail(TR_ERR_UNSUPPORTED, "total_tokens = %lld, n_channels = %d are too large", (long long)T, C);
+  if (!known_dtype(dtype) || !known_dtype(gate_dtype)) return fail(TR_ERR_DTYPE, "dtype/gate_dtype");
+  if (flags & ~(unsigned)TR_GATE_LOGITS) return fail(TR_ERR_INVALID_ARG, "unknown recurrence flags 0x%x", flags);
+  if (!cu) return fail(TR_ERR_INVALID_ARG, "cu_seqlens is NULL");
+  if (!aligned4(cu)) return fail(TR_ERR_ALIGNMENT, "cu_seqlens must be 4-byte aligned");
+  return check_cu_host(cu_host, n_seqs, T);
+}
+
+// a [T, C] operand: element-aligned rows, at least C apart (0: packed)
+tr_status check_rows(const void *p, int64_t *stride, int32_t C, int64_t T, int esz, const char *what) {
+  if (*stride == 0) *stride = C;
+  if (*stride < C) return fail(TR_ERR_SHAPE, "%s: the token stride is smaller than the row", what);
+  if (!p && T > 0) return fail(TR_ERR_INVALID_ARG, "%s is NULL", what);
+  if (!aligned_to(p, esz)) return fail(TR_ERR_ALIGNMENT, "%s must be aligned to its elements", what);
+  return TR_OK;
+}
+
+}  // namespace
+
+tr_status tr_linear_recurrence(const tr_recurrence_args *a, void *stream) {
+  if (!a) return fail(TR_ERR_INVALID_ARG, "args is NULL");
+  tr_status st = check_recurrence(a->n_seqs, a->n_channels, a->total_tokens, a->dtype, a->gate_dtype, a->flags,
+                                  a->cu_seqlens, a->cu_seqlens_host);
+  if (st != TR_OK) return st;
+  tr::RecurrenceLaunch p{};
+  p.n_seqs = a->n_seqs;
+  p.C = a->n_channels;
+  p.T = a->total_tokens;
+  p.x_bf16 = a->dtype == TR_DTYPE_BF16;
+  p.gate_bf16 = a->gate_dtype == TR_DTYPE_BF16;
+  p.logits = (a->flags & TR_GATE_LOGITS) != 0;
+  p.x_stride = a->x_stride;
+  p.gate_stride = a->gate_stride;
+  p.y_stride = a->y_stride;
+  const int xs = dtype_size(a->dtype), gs = dtype_size(a->gate_dtype);
+  if ((st = check_rows(a->x, &p.x_stride, p.C, p.T, xs, "x")) != TR_OK ||
+      (st = check_rows(a->gate, &p.gate_stride, p.C, p.T, gs, "gate")) != TR_OK ||
+      (st = check_rows(a->y, &p.y_stride, p.C, 0, xs, "y")) != TR_OK)
+    return st;
+  if (p.T > 0 && a->y && (a->y == a->x || a->y == a->gate)) return fail(TR_ERR_INVALID_ARG, "y aliases an input");
+  if (!a->h_final && a->n_seqs > 0) return fail(TR_ERR_INVALID_ARG, "h_final is NULL");
+  if (!aligned4(a->h0) || !aligned4(a->h_final)) return fail(TR_ERR_ALIGNMENT, "h0/h_final must be 4-byte aligned");
+  p.x = a->x;
+  p.gate = a->gate;
+  p.cu = a->cu_seqlens;
+  p.cu_host = a->cu_seqlens_host;
+  p.h0 = a->h0;
+  p.y = a->y;
+  p.h_final = a->h_final;
+  cudaError_t e = tr::launch_recurrence(p, static_cast<cudaStream_t>(stream), true);
+  if (e != cudaSuccess) return cuda_fail(e, "linear recurrence");
+  return ok();
+}
+
+tr_status tr_linear_recurrence_backward(const tr_recurrence_grad_args *a, void *stream) {
+  if (!a) return fail(TR_ERR_INVALID_ARG, "args is NULL");
+  tr_status st = check_recurrence(a->n_seqs, a->n_channels, a->total_tokens, a->dtype, a->gate_dtype, a->flags,
+                                  a->cu_seqlens, a->cu_seqlens_host);
+  if (st != TR_OK) return st;
+  tr::RecurrenceGradLaunch p{};
+  p.n_seqs = a->n_seqs;
+  p.C = a->n_channels;
+  p.T = a->total_tokens;
+  p.x_bf16 = a->dtype == TR_DTYPE_BF16;
+  p.gate_bf16 = a->gate_dtype == TR_DTYPE_BF16;
+  p.logits = (a->flags & TR_GATE_LOGITS) != 0;
+  p.dy_stride = a->dy_stride;
+  p.gate_stride = a->gate_stride;
+  p.y_stride = a->y_stride;
+  p.dx_stride = a->dx_stride;
+  p.dgate_stride = a->dgate_stride;
+  const int xs = dtype_size(a->dtype), gs = dtype_size(a->gate_dtype);
+  if ((st = check_rows(a->dy, &p.dy_stride, p.C, p.T, xs, "dy")) != TR_OK ||
+      (st = check_rows(a->gate, &p.gate_stride, p.C, p.T, gs, "gate")) != TR_OK ||
+      (st = check_rows(a->y, &p.y_stride, p.C, p.T, xs, "y")) != TR_OK ||
+      (st = check_rows(a->dx, &p.dx_stride, p.C, p.T, xs, "dx")) != TR_OK ||
+      (st = check_rows(a->dgate, &p.dgate_stride, p.C, p.T, gs, "dgate")) != TR_OK)
+    return st;
+  const void *in[3] = {a->dy, a->gate, a->y};
+  for (const void *i : in)
+    if (p.T > 0 && (a->dx == i || a->dgate == i)) return fail(TR_ERR_INVALID_ARG, "a gradient aliases an input");
+  if (p.T > 0 && a->dx == a->dgate) return fail(TR_ERR_INVALID_ARG, "dx aliases dgate");
+  if (!aligned4(a->h0) || !aligned4(a->dh_final) || !aligned4(a->dh0))
+    return fail(TR_ERR_ALIGNMENT, "h0/dh_final/dh0 must be 4-byte aligned");
+  p.dy = a->dy;
+  p.gate = a->gate;
+  p.y = a->y;
+  p.cu = a->cu_seqlens;
+  p.cu_host = a->cu_seqlens_host;
+  p.h0 = a->h0;
+  p.dh_final = a->dh_final;
+  p.dx = a->dx;
+  p.dgate = a->dgate;
+  p.dh0 = a->dh0;
+  cudaError_t e = tr::launch_recurrence_grad(p, static_cast<cudaStream_t>(stream), true);
+  if (e != cudaSuccess) return cuda_fail(e, "linear recurrence (backward)");
   return ok();
 }
 
