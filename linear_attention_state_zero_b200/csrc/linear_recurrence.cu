@@ -24,9 +24,9 @@
 
 #include <algorithm>
 
+#include "fp8_ptx.cuh"
 #include "layer_ops.h"
 #include "tr_internal.h"
-#include "tr_ptx.cuh"
 
 namespace tr {
 namespace {
@@ -82,29 +82,6 @@ __device__ __forceinline__ float decay(float g, float &rest) {
   const float a = __fdividef(1.f, 1.f + e);
   rest = e * a;
   return a;
-}
-
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ uint32_t cluster_size() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_arrive() {
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void cluster_wait() {
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void st_cluster(uint32_t local, uint32_t rank, float v) {
-  asm volatile(
-      "{\n\t.reg .b32 r;\n\tmapa.shared::cluster.u32 r, %0, %1;\n\t"
-      "st.shared::cluster.f32 [r], %2;\n\t}" ::"r"(local), "r"(rank), "f"(v)
-      : "memory");
 }
 
 // The maps of a round: per warp of this CTA, and per CTA of the cluster (two sets, used in
