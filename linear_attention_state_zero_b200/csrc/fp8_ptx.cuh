@@ -126,8 +126,8 @@ __device__ __forceinline__ uint32_t cluster_map(uint32_t local, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(local), "r"(rank));
   return r;
 }
-__device__ __forceinline__ void st_cluster(uint32_t local, uint32_t rank, float v) {
-  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_map(local, rank)), "f"(v) : "memory");
+__device__ __forceinline__ void st_cluster(uint32_t cluster_addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_addr), "f"(v) : "memory");
 }
 // Arrive on an mbarrier of any CTA of the cluster (a shared::cluster address) without ordering
 // other memory accesses: what the waiter reuses is tensor memory whose loads have completed

@@ -36,61 +36,88 @@ constexpr int kMaxParts = 64;     // independent runs of whole sequences (grid.y
 constexpr int kMaxCluster = 8;
 
 struct Parts {
-  int32_t at[kMaxParts + 1];      // token bounds of the runs, each at a sequence start
+  int32_t lo[kMaxParts], hi[kMaxParts];   // tokens of each run, the longest first
 };
+
+template <int V> struct alignas(4 * V) Floats { float f[V]; };
 
 // V channels of one token as loaded
 template <typename T, int V> struct Raw;
 template <> struct Raw<__nv_bfloat16, 1> { unsigned short u; };
-template <> struct Raw<__nv_bfloat16, 2> { uint32_t u; };
-template <> struct Raw<float, 1> { float f; };
-template <> struct Raw<float, 2> { float2 f; };
+template <> struct Raw<__nv_bfloat16, 2> { uint32_t u[1]; };
+template <> struct alignas(8) Raw<__nv_bfloat16, 4> { uint32_t u[2]; };
+template <int V> struct Raw<float, V> : Floats<V> {};
 
 template <typename T, int V>
-__device__ __forceinline__ Raw<T, V> ld_raw(const void *p, int64_t off, bool in) {
-  Raw<T, V> r{};
-  if (in) r = *reinterpret_cast<const Raw<T, V> *>(reinterpret_cast<const T *>(p) + off);
-  return r;
+__device__ __forceinline__ Raw<T, V> ld_raw(const T *p) {
+  return *reinterpret_cast<const Raw<T, V> *>(p);
 }
 __device__ __forceinline__ void to_f32(const Raw<__nv_bfloat16, 1> &r, float (&f)[1]) {
   f[0] = __uint_as_float((uint32_t)r.u << 16);
 }
-__device__ __forceinline__ void to_f32(const Raw<__nv_bfloat16, 2> &r, float (&f)[2]) {
-  f[0] = __uint_as_float(r.u << 16);
-  f[1] = __uint_as_float(r.u & 0xffff0000u);
+template <int V>
+__device__ __forceinline__ void to_f32(const Raw<__nv_bfloat16, V> &r, float (&f)[V]) {
+#pragma unroll
+  for (int v = 0; v < V; v += 2) {
+    f[v] = __uint_as_float(r.u[v / 2] << 16);
+    f[v + 1] = __uint_as_float(r.u[v / 2] & 0xffff0000u);
+  }
 }
-__device__ __forceinline__ void to_f32(const Raw<float, 1> &r, float (&f)[1]) { f[0] = r.f; }
-__device__ __forceinline__ void to_f32(const Raw<float, 2> &r, float (&f)[2]) {
-  f[0] = r.f.x;
-  f[1] = r.f.y;
+template <int V>
+__device__ __forceinline__ void to_f32(const Raw<float, V> &r, float (&f)[V]) {
+#pragma unroll
+  for (int v = 0; v < V; ++v) f[v] = r.f[v];
 }
 __device__ __forceinline__ void st_f32(__nv_bfloat16 *p, const float (&f)[1]) { *p = __float2bfloat16_rn(f[0]); }
-__device__ __forceinline__ void st_f32(__nv_bfloat16 *p, const float (&f)[2]) {
-  *reinterpret_cast<uint32_t *>(p) = pack_bf16x2(f[0], f[1]);
+template <int V>
+__device__ __forceinline__ void st_f32(__nv_bfloat16 *p, const float (&f)[V]) {
+  Raw<__nv_bfloat16, V> r;
+#pragma unroll
+  for (int v = 0; v < V; v += 2) r.u[v / 2] = pack_bf16x2(f[v], f[v + 1]);
+  *reinterpret_cast<Raw<__nv_bfloat16, V> *>(p) = r;
 }
-__device__ __forceinline__ void st_f32(float *p, const float (&f)[1]) { *p = f[0]; }
-__device__ __forceinline__ void st_f32(float *p, const float (&f)[2]) {
-  *reinterpret_cast<float2 *>(p) = make_float2(f[0], f[1]);
+template <int V>
+__device__ __forceinline__ void st_f32(float *p, const float (&f)[V]) {
+  Floats<V> r;
+#pragma unroll
+  for (int v = 0; v < V; ++v) r.f[v] = f[v];
+  *reinterpret_cast<Floats<V> *>(p) = r;
 }
 
-// a, and for the backward pass 1 - a where the gate is a logit.  Above 80 e^gate is held at
-// e^80 (a < 2e-35); the comparison keeps a NaN.
+__device__ __forceinline__ float rcp_ftz(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// a.  (e^gate may be infinite: a is 0 then.)
 template <bool LOGITS>
-__device__ __forceinline__ float decay(float g, float &rest) {
-  if (!LOGITS) return exp_ftz(g);
-  const float e = exp_ftz(g > 80.f ? 80.f : g);
-  const float a = __fdividef(1.f, 1.f + e);
-  rest = e * a;
+__device__ __forceinline__ float decay(float g) {
+  return LOGITS ? rcp_ftz(1.f + exp_ftz(g)) : exp_ftz(g);
+}
+// a, and w = d(log a) / d(gate): 1, or -(1 - a) = -a e^gate for a logit.  Above 80, e^gate is held
+// at e^80 (a < 2e-35), so that the product stays finite; the minimum keeps a NaN.
+template <bool LOGITS>
+__device__ __forceinline__ float decay(float g, float &w) {
+  if (!LOGITS) {
+    w = 1.f;
+    return exp_ftz(g);
+  }
+  float c;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(c) : "f"(g), "f"(80.f));
+  const float e = exp_ftz(c), a = rcp_ftz(1.f + e);
+  w = -e * a;
   return a;
 }
 
-// The maps of a round: per warp of this CTA, and per CTA of the cluster (two sets, used in
-// turn: the barrier of a round is passed only when every reader of the round before is done).
+// A map u -> A u + B per channel; `start`: a sequence begins inside, so u does not count.
 template <int V>
 struct Maps {
-  float A[V][32], B[V][32];
-  float start;                     // 1: a sequence begins inside, so A does not count
+  Floats<V> A[32], B[32];
+  float start;
 };
+// The maps of a round: per warp of this CTA, and per CTA of the cluster (two sets, used in
+// turn: the barrier of a round is passed only when every reader of the round before is done).
 template <int V>
 struct Shared {
   Maps<V> warp[2][kW];
@@ -98,13 +125,13 @@ struct Shared {
 };
 
 // Where sequences begin in tokens [t0, t0 + n], n <= 31: bit i for a cu entry equal to t0 + i
-// (cu[N] = T among them); first = the last sequence with cu <= t0.  `hint` is a sequence known
-// to begin at or before t0.  The whole warp calls it with the same arguments.
+// (cu[N] = T among them); first = the last sequence with cu <= t0.  The whole warp calls it with
+// the same arguments.
 __device__ __forceinline__ uint32_t starts_mask(const int32_t *__restrict__ cu, int n_seqs, int t0,
-                                                int n, int hint, int &first) {
+                                                int n, int &first) {
   const int lane = threadIdx.x & 31;
-  // the last index in [lo, n_seqs] with cu <= t0, 32 probes a step
-  int lo = hint, hi = n_seqs + 1;             // cu[lo] <= t0, cu[hi] > t0 (hi: past the end)
+  // the last index in [0, n_seqs] with cu <= t0, 32 probes a step
+  int lo = 0, hi = n_seqs + 1;                // cu[lo] <= t0, cu[hi] > t0 (hi: past the end)
   while (hi - lo > 1) {
     const int step = (hi - lo + 31) / 32;
     const int at = lo + (lane + 1) * step;    // lane 31 is at or past hi
@@ -124,79 +151,87 @@ __device__ __forceinline__ uint32_t starts_mask(const int32_t *__restrict__ cu, 
   return __reduce_or_sync(0xffffffffu, m);
 }
 
-// u after the map (A, B), or after a segment in which a sequence begins
-__device__ __forceinline__ float apply(float A, float B, float start, float u) {
-  return start != 0.f ? B : fmaf(A, u, B);
-}
-
-// Joins the warps' maps of a round.  In: this warp's map.  Out: the value in front of this
-// warp's segment; `carry` (the value in front of the round) moves to the next round.
+// Joins the maps of a round.  In: this warp's map.  Out: the value in front of this warp's
+// segment; `carry` (the value in front of the round) moves to the next round.
 template <int V>
 __device__ __forceinline__ void join(Shared<V> &sh, int par, uint32_t S, uint32_t r, const float (&A)[V],
                                      const float (&B)[V], bool start, float (&carry)[V], float (&u)[V]) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   Maps<V> &mine = sh.warp[par][warp];
+  Floats<V> fa, fb;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    mine.A[v][lane] = A[v];
-    mine.B[v][lane] = B[v];
+    fa.f[v] = A[v];
+    fb.f[v] = B[v];
   }
+  mine.A[lane] = fa;
+  mine.B[lane] = fb;
   if (lane == 0) mine.start = start ? 1.f : 0.f;
-  __syncthreads();
-  if (S > 1) {
-    if (warp == 0) {
-      float a[V], b[V], st = 0.f;
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        a[v] = 1.f;
-        b[v] = 0.f;
-      }
-#pragma unroll
-      for (int w = 0; w < kW; ++w) {
-        const Maps<V> &m = sh.warp[par][w];
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          b[v] = apply(m.A[v][lane], m.B[v][lane], m.start, b[v]);
-          a[v] *= m.A[v][lane];
-        }
-        st = m.start != 0.f ? 1.f : st;
-      }
-      Maps<V> &to = sh.cta[par][r];
-      for (uint32_t k = 0; k < S; ++k) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          st_cluster(smem_u32(&to.A[v][lane]), k, a[v]);
-          st_cluster(smem_u32(&to.B[v][lane]), k, b[v]);
-        }
-        if (lane == 0) st_cluster(smem_u32(&to.start), k, st);
-      }
-    }
-    __syncwarp();
-    cluster_arrive();
-    cluster_wait();
-    for (uint32_t k = 0; k < S; ++k) {
-      const Maps<V> &m = sh.cta[par][k];
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        if (k == r) u[v] = carry[v];
-        carry[v] = apply(m.A[v][lane], m.B[v][lane], m.start, carry[v]);
-      }
-    }
-  } else {
-#pragma unroll
-    for (int v = 0; v < V; ++v) u[v] = carry[v];
+  const bool any = __syncthreads_or(start);
+  if (S == 1) {
 #pragma unroll
     for (int w = 0; w < kW; ++w) {
       const Maps<V> &m = sh.warp[par][w];
+      const Floats<V> ma = m.A[lane], mb = m.B[lane];
+      const bool st = any && m.start != 0.f;
 #pragma unroll
-      for (int v = 0; v < V; ++v)
-        carry[v] = apply(m.A[v][lane], m.B[v][lane], m.start, carry[v]);
+      for (int v = 0; v < V; ++v) {
+        if (w == warp) u[v] = carry[v];
+        carry[v] = st ? mb.f[v] : fmaf(ma.f[v], carry[v], mb.f[v]);
+      }
+    }
+    return;
+  }
+  // the CTA's map up to this warp's segment (pa, pb, ps) and in all (ta, tb, ts)
+  float ta[V], tb[V], pa[V], pb[V];
+  bool ts = false, ps = false;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    ta[v] = pa[v] = 1.f;
+    tb[v] = pb[v] = 0.f;
+  }
+#pragma unroll
+  for (int w = 0; w < kW; ++w) {
+    const Maps<V> &m = sh.warp[par][w];
+    const Floats<V> ma = m.A[lane], mb = m.B[lane];
+    const bool st = any && m.start != 0.f;
+    if (w == warp) ps = ts;
+    ts = ts || st;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      if (w == warp) {
+        pa[v] = ta[v];
+        pb[v] = tb[v];
+      }
+      tb[v] = st ? mb.f[v] : fmaf(ma.f[v], tb[v], mb.f[v]);
+      ta[v] *= ma.f[v];
     }
   }
-  for (int w = 0; w < warp; ++w) {
-    const Maps<V> &m = sh.warp[par][w];
+  if (warp < (int)S) {   // warp k tells CTA k
+    Maps<V> &to = sh.cta[par][r];
+    const uint32_t da = cluster_map(smem_u32(&to.A[lane]), (uint32_t)warp);
+    const uint32_t db = cluster_map(smem_u32(&to.B[lane]), (uint32_t)warp);
 #pragma unroll
-    for (int v = 0; v < V; ++v) u[v] = apply(m.A[v][lane], m.B[v][lane], m.start, u[v]);
+    for (int v = 0; v < V; ++v) {
+      st_cluster(da + 4 * v, ta[v]);
+      st_cluster(db + 4 * v, tb[v]);
+    }
+    if (lane == 0) st_cluster(cluster_map(smem_u32(&to.start), (uint32_t)warp), ts ? 1.f : 0.f);
+  }
+  __syncwarp();
+  cluster_arrive();
+  cluster_wait();
+#pragma unroll
+  for (uint32_t k = 0; k < kMaxCluster; ++k) {
+    if (k >= S) break;
+    const Maps<V> &m = sh.cta[par][k];
+    const Floats<V> ma = m.A[lane], mb = m.B[lane];
+    const bool st = m.start != 0.f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      if (k == r) u[v] = ps ? pb[v] : fmaf(pa[v], carry[v], pb[v]);
+      carry[v] = st ? mb.f[v] : fmaf(ma.f[v], carry[v], mb.f[v]);
+    }
   }
 }
 
@@ -213,6 +248,9 @@ __device__ __forceinline__ void copy_empty(const int32_t *__restrict__ cu, int n
   }
 }
 
+// Registers bound it: 32 elements of a segment per thread at two bytes (16 at four) are 64 for
+// the segment in hand and 32 for the next one's loads, which with two CTAs keep 64 KB in flight
+// on each SM.
 template <typename TX, typename TG, bool LOGITS, int V, int LS>
 __global__ void __launch_bounds__(kW * 32, 2) recurrence_kernel(RecurrenceLaunch p, Parts parts) {
   __shared__ Shared<V> sh;
@@ -220,7 +258,7 @@ __global__ void __launch_bounds__(kW * 32, 2) recurrence_kernel(RecurrenceLaunch
   const uint32_t S = cluster_size(), r = cluster_rank();
   const int c = (int)(blockIdx.x / S) * 32 * V + lane * V;
   const bool live = c < p.C;
-  const int tb = parts.at[blockIdx.y], te = parts.at[blockIdx.y + 1];
+  const int tb = parts.lo[blockIdx.y], te = parts.hi[blockIdx.y];
   const int chunk = (int)S * kW * LS;
   pdl_trigger();
   if (S > 1) {   // every CTA of the cluster has started before any writes to it
@@ -230,53 +268,70 @@ __global__ void __launch_bounds__(kW * 32, 2) recurrence_kernel(RecurrenceLaunch
   pdl_wait();
   copy_empty<V>(p.cu, p.n_seqs, (int)((blockIdx.y * S + r) * kW) + warp, (int)(gridDim.y * S * kW), c,
                 live, p.C, p.h0, p.h_final);
+  // lanes past the last channel load the last ones and store nothing
+  const int cl = live ? c : p.C - V;
+  const bool put_y = live && p.y;
+  int t0 = tb + (int)r * kW * LS + warp * LS;
+  const TX *px = reinterpret_cast<const TX *>(p.x) + (int64_t)t0 * p.x_stride + cl;
+  const TG *pg = reinterpret_cast<const TG *>(p.gate) + (int64_t)t0 * p.gate_stride + cl;
+  TX *py = reinterpret_cast<TX *>(p.y) + (int64_t)t0 * p.y_stride + cl;
   Raw<TX, V> nx[LS];
   Raw<TG, V> ng[LS];
-  const int seg0 = (int)r * kW * LS + warp * LS;
-  auto fetch = [&](int t0) {
+  auto fetch = [&](int left) {   // the segment at px, pg, of which `left` tokens exist
+    if (left >= LS) {
 #pragma unroll
-    for (int i = 0; i < LS; ++i) {
-      const bool in = live && t0 + i < te;
-      nx[i] = ld_raw<TX, V>(p.x, (int64_t)(t0 + i) * p.x_stride + c, in);
-      ng[i] = ld_raw<TG, V>(p.gate, (int64_t)(t0 + i) * p.gate_stride + c, in);
+      for (int i = 0; i < LS; ++i) {
+        nx[i] = ld_raw<TX, V>(px + i * p.x_stride);
+        ng[i] = ld_raw<TG, V>(pg + i * p.gate_stride);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < LS; ++i) {
+        nx[i] = i < left ? ld_raw<TX, V>(px + i * p.x_stride) : Raw<TX, V>{};
+        ng[i] = i < left ? ld_raw<TG, V>(pg + i * p.gate_stride) : Raw<TG, V>{};
+      }
     }
+    px += chunk * p.x_stride;
+    pg += chunk * p.gate_stride;
   };
   float carry[V] = {};
-  int hint = 0, par = 0;
-  fetch(tb + seg0);
-  for (int tr0 = tb; tr0 < te; tr0 += chunk, par ^= 1) {
-    const int t0 = tr0 + seg0;
+  int par = 0, seq = 0, from = 1, to = 0;   // the sequence that was looked up last: its tokens
+  fetch(te - t0);
+#pragma unroll 1
+  for (int tr0 = tb; tr0 < te; tr0 += chunk, t0 += chunk, py += chunk * p.y_stride, par ^= 1) {
     const int lim = te - t0 < LS ? te - t0 : LS;    // tokens of the segment (may be <= 0)
     float a[LS][V], x[LS][V];
 #pragma unroll
     for (int i = 0; i < LS; ++i) {
-      float g[V], rest;
+      float g[V];
       to_f32(nx[i], x[i]);
       to_f32(ng[i], g);
 #pragma unroll
-      for (int v = 0; v < V; ++v) a[i][v] = decay<LOGITS>(g[v], rest);
+      for (int v = 0; v < V; ++v) a[i][v] = decay<LOGITS>(g[v]);
     }
-    if (te - tr0 > chunk) fetch(t0 + chunk);
-    int seq = 0;
-    const uint32_t mask = lim > 0 ? starts_mask(p.cu, p.n_seqs, t0, LS, hint, seq) : 0u;
-    hint = lim > 0 ? seq : hint;
-    const uint32_t inside = mask & ((1u << (lim > 0 ? lim : 0)) - 1u);
-    const int first = inside ? __ffs(inside) - 1 : lim;   // tokens of the sequence before
+    fetch(te - t0 - chunk);
+    uint32_t mask = 0;
+    if (lim > 0 && (t0 <= from || t0 + LS >= to)) {
+      mask = starts_mask(p.cu, p.n_seqs, t0, LS, seq);
+      from = __ldg(p.cu + seq);
+      to = __ldg(p.cu + seq + 1);
+    }
+    const bool whole = lim == LS && (mask & ~(1u << LS)) == 0;   // of one sequence, begun before
     float A[V], B[V], u[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       A[v] = 1.f;
       B[v] = 0.f;
     }
-    auto put = [&](int t, const float (&h)[V]) {
-      if (p.y && live) st_f32(reinterpret_cast<TX *>(p.y) + (int64_t)t * p.y_stride + c, h);
+    auto put = [&](int i, const float (&h)[V]) {
+      if (put_y) st_f32(py + i * p.y_stride, h);
     };
     auto put_final = [&](int n, const float (&h)[V]) {
       if (!live) return;
 #pragma unroll
       for (int v = 0; v < V; ++v) p.h_final[(int64_t)n * p.C + c + v] = h[v];
     };
-    if (first == LS) {
+    if (whole) {
 #pragma unroll
       for (int i = 0; i < LS; ++i)
 #pragma unroll
@@ -284,7 +339,17 @@ __global__ void __launch_bounds__(kW * 32, 2) recurrence_kernel(RecurrenceLaunch
           B[v] = fmaf(a[i][v], B[v], x[i][v]);
           A[v] *= a[i][v];
         }
+      join<V>(sh, par, S, r, A, B, false, carry, u);
+#pragma unroll
+      for (int i = 0; i < LS; ++i) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) u[v] = fmaf(a[i][v], u[v], x[i][v]);
+        put(i, u);
+      }
+      if (mask >> LS) put_final(seq, u);
     } else {
+      const uint32_t inside = mask & ((1u << (lim > 0 ? lim : 0)) - 1u);
+      const int first = inside ? __ffs(inside) - 1 : lim;   // tokens of the sequence before
       // from the first sequence start on, the states do not depend on what lies before the
       // segment: they are final here
       int n = seq;
@@ -304,30 +369,47 @@ __global__ void __launch_bounds__(kW * 32, 2) recurrence_kernel(RecurrenceLaunch
           }
         }
         if (i >= first) {
-          put(t0 + i, B);
+          put(i, B);
           if (mask >> (i + 1) & 1u) put_final(n, B);
         }
       }
-    }
-    join<V>(sh, par, S, r, A, B, inside != 0, carry, u);
-    if (first == LS) {
-#pragma unroll
-      for (int i = 0; i < LS; ++i) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) u[v] = fmaf(a[i][v], u[v], x[i][v]);
-        put(t0 + i, u);
-      }
-      if (mask >> LS & 1u) put_final(seq, u);
-    } else {
+      join<V>(sh, par, S, r, A, B, inside != 0, carry, u);
 #pragma unroll
       for (int i = 0; i < LS; ++i) {
         if (i >= first) continue;
 #pragma unroll
         for (int v = 0; v < V; ++v) u[v] = fmaf(a[i][v], u[v], x[i][v]);
-        put(t0 + i, u);
+        put(i, u);
         if (mask >> (i + 1) & 1u) put_final(seq, u);
       }
     }
+  }
+}
+
+// Sequences of at most one token (decoding): h_final = a h0 + x, a thread per V channels.
+template <typename TX, typename TG, bool LOGITS, int V>
+__global__ void __launch_bounds__(256) recurrence_step_kernel(RecurrenceLaunch p) {
+  const int per = (p.C + 256 * V - 1) / (256 * V);   // blocks per sequence
+  pdl_trigger();
+  pdl_wait();
+  for (int64_t b = blockIdx.x; b < (int64_t)p.n_seqs * per; b += gridDim.x) {
+    const int n = (int)(b / per);
+    const int c = ((int)(b - (int64_t)n * per) * 256 + (int)threadIdx.x) * V;
+    if (c >= p.C) continue;
+    const int t = __ldg(p.cu + n);
+    const bool some = __ldg(p.cu + n + 1) > t;
+    const int64_t hc = (int64_t)n * p.C + c;
+    float h[V] = {};
+    if (p.h0) to_f32(ld_raw<float, V>(p.h0 + hc), h);
+    if (some) {
+      float x[V], g[V];
+      to_f32(ld_raw<TX, V>(reinterpret_cast<const TX *>(p.x) + t * p.x_stride + c), x);
+      to_f32(ld_raw<TG, V>(reinterpret_cast<const TG *>(p.gate) + t * p.gate_stride + c), g);
+#pragma unroll
+      for (int v = 0; v < V; ++v) h[v] = p.h0 ? fmaf(decay<LOGITS>(g[v]), h[v], x[v]) : x[v];
+      if (p.y) st_f32(reinterpret_cast<TX *>(p.y) + t * p.y_stride + c, h);
+    }
+    st_f32(p.h_final + hc, h);
   }
 }
 
@@ -340,7 +422,7 @@ __global__ void __launch_bounds__(kW * 32, 2) recurrence_grad_kernel(RecurrenceG
   const uint32_t S = cluster_size(), r = cluster_rank();
   const int c = (int)(blockIdx.x / S) * 32 * V + lane * V;
   const bool live = c < p.C;
-  const int tb = parts.at[blockIdx.y], te = parts.at[blockIdx.y + 1];
+  const int tb = parts.lo[blockIdx.y], te = parts.hi[blockIdx.y];
   const int chunk = (int)S * kW * LS;
   pdl_trigger();
   if (S > 1) {
@@ -351,48 +433,80 @@ __global__ void __launch_bounds__(kW * 32, 2) recurrence_grad_kernel(RecurrenceG
   if (p.dh0)
     copy_empty<V>(p.cu, p.n_seqs, (int)((blockIdx.y * S + r) * kW) + warp, (int)(gridDim.y * S * kW),
                   c, live, p.C, p.dh_final, p.dh0);
-  Raw<TX, V> nd[LS], ny[LS];
+  const int cl = live ? c : p.C - V;
+  int t1 = te - 1 - ((int)r * kW * LS + warp * LS);
+  const TX *pd = reinterpret_cast<const TX *>(p.dy) + (int64_t)t1 * p.dy_stride + cl;
+  const TG *pg = reinterpret_cast<const TG *>(p.gate) + (int64_t)t1 * p.gate_stride + cl;
+  const TX *ph = reinterpret_cast<const TX *>(p.y) + (int64_t)(t1 - 1) * p.y_stride + cl;   // h_{t-1}
+  TX *ox = reinterpret_cast<TX *>(p.dx) + (int64_t)t1 * p.dx_stride + cl;
+  TG *og = reinterpret_cast<TG *>(p.dgate) + (int64_t)t1 * p.dgate_stride + cl;
+  Raw<TX, V> nd[LS], nh[LS];
   Raw<TG, V> ng[LS];
-  const int seg0 = (int)r * kW * LS + warp * LS;
-  auto fetch = [&](int t1) {
+  auto fetch = [&](int left) {
+    if (left > LS) {
 #pragma unroll
-    for (int i = 0; i < LS; ++i) {
-      const int t = t1 - i;
-      const bool in = live && t >= tb;
-      nd[i] = ld_raw<TX, V>(p.dy, (int64_t)t * p.dy_stride + c, in);
-      ng[i] = ld_raw<TG, V>(p.gate, (int64_t)t * p.gate_stride + c, in);
-      ny[i] = ld_raw<TX, V>(p.y, (int64_t)(t - 1) * p.y_stride + c, in && t > tb);
-    }
-  };
-  float carry[V] = {};
-  int par = 0;
-  fetch(te - 1 - seg0);
-  for (int tr1 = te - 1; tr1 >= tb; tr1 -= chunk, par ^= 1) {
-    const int t1 = tr1 - seg0;
-    const int lim = t1 - tb + 1 < LS ? t1 - tb + 1 : LS;
-    float a[LS][V], w[LS][V], d[LS][V], hp[LS][V];   // w = d(log a)/d(gate)
+      for (int i = 0; i < LS; ++i) {
+        nd[i] = ld_raw<TX, V>(pd - i * p.dy_stride);
+        ng[i] = ld_raw<TG, V>(pg - i * p.gate_stride);
+        nh[i] = ld_raw<TX, V>(ph - i * p.y_stride);
+      }
+    } else {
 #pragma unroll
-    for (int i = 0; i < LS; ++i) {
-      float g[V];
-      to_f32(nd[i], d[i]);
-      to_f32(ny[i], hp[i]);
-      to_f32(ng[i], g);
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        a[i][v] = decay<LOGITS>(g[v], w[i][v]);
-        if (LOGITS) w[i][v] = -w[i][v];
+      for (int i = 0; i < LS; ++i) {
+        nd[i] = i < left ? ld_raw<TX, V>(pd - i * p.dy_stride) : Raw<TX, V>{};
+        ng[i] = i < left ? ld_raw<TG, V>(pg - i * p.gate_stride) : Raw<TG, V>{};
+        nh[i] = i < left - 1 ? ld_raw<TX, V>(ph - i * p.y_stride) : Raw<TX, V>{};
       }
     }
-    if (tr1 - tb >= chunk) fetch(t1 - chunk);
+    pd -= chunk * p.dy_stride;
+    pg -= chunk * p.gate_stride;
+    ph -= chunk * p.y_stride;
+  };
+  float carry[V] = {};
+  int par = 0, seq = 0, from = 1, to = 0;
+  fetch(t1 - tb + 1);
+#pragma unroll 1
+  for (int tr1 = te - 1; tr1 >= tb;
+       tr1 -= chunk, t1 -= chunk, ox -= chunk * p.dx_stride, og -= chunk * p.dgate_stride, par ^= 1) {
+    const int lim = t1 - tb + 1 < LS ? t1 - tb + 1 : LS;
     // starts of the tokens [t0, t1 + 1]: token t ends its sequence when t + 1 starts one
     const int t0 = t1 - lim + 1;
-    int seq = 0;
-    const uint32_t mask = lim > 0 ? starts_mask(p.cu, p.n_seqs, t0, lim, 0, seq) : 0u;
+    uint32_t mask = 0;
+    if (lim > 0 && (t0 <= from || t1 + 1 >= to)) {
+      mask = starts_mask(p.cu, p.n_seqs, t0, lim, seq);
+      from = __ldg(p.cu + seq);
+      to = __ldg(p.cu + seq + 1);
+    }
+    // the sequence that holds token t (t0 <= t <= t1): the last one that begins at or before it
+    auto seq_of = [&](int t) {
+      int n = seq;
+      while (n + 1 < p.n_seqs && __ldg(p.cu + n + 1) <= t) ++n;
+      return n;
+    };
     // bit i: token t1 - i ends (begins) a sequence
     const uint32_t rev = lim > 0 ? __brev(mask) >> (31 - lim) : 0u;  // bit j: t0 + lim - j starts
     const uint32_t ends = rev & ((1u << (lim > 0 ? lim : 0)) - 1u);
     const uint32_t begins = rev >> 1;
-    const int first = ends ? __ffs(ends) - 1 : lim;
+    float a[LS][V], d[LS][V], q[LS][V];   // q = h_{t-1} d(log a)/d(gate)
+#pragma unroll
+    for (int i = 0; i < LS; ++i) {
+      float g[V], h[V];
+      to_f32(nd[i], d[i]);
+      to_f32(nh[i], h);
+      to_f32(ng[i], g);
+      if (begins >> i & 1u) {
+        const int n = seq_of(t1 - i);
+#pragma unroll
+        for (int v = 0; v < V; ++v) h[v] = p.h0 && live ? p.h0[(int64_t)n * p.C + c + v] : 0.f;
+      }
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        float w;
+        a[i][v] = decay<LOGITS>(g[v], w);
+        q[i][v] = h[v] * w;
+      }
+    }
+    fetch(t1 - tb + 1 - chunk);
     float A[V], B[V], u[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -400,38 +514,26 @@ __global__ void __launch_bounds__(kW * 32, 2) recurrence_grad_kernel(RecurrenceG
       B[v] = 0.f;
     }
     // the token's gradients; on entry u is what reaches h_t from behind, on exit u_t
-    auto emit = [&](int i, float (&uu)[V], int n) {
-      const int t = t1 - i;
+    auto emit = [&](int i, float (&uu)[V]) {
       float G[V], dg[V];
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         G[v] = d[i][v] + uu[v];
         uu[v] = a[i][v] * G[v];
-      }
-      const bool begin = begins >> i & 1u;
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        float h = hp[i][v];
-        if (begin) h = p.h0 && live ? p.h0[(int64_t)n * p.C + c + v] : 0.f;
-        dg[v] = uu[v] * h;
-        if (LOGITS) dg[v] *= w[i][v];
+        dg[v] = uu[v] * q[i][v];
       }
       if (live) {
-        st_f32(reinterpret_cast<TX *>(p.dx) + (int64_t)t * p.dx_stride + c, G);
-        st_f32(reinterpret_cast<TG *>(p.dgate) + (int64_t)t * p.dgate_stride + c, dg);
-        if (begin && p.dh0) {
-#pragma unroll
-          for (int v = 0; v < V; ++v) p.dh0[(int64_t)n * p.C + c + v] = uu[v];
-        }
+        st_f32(ox - i * p.dx_stride, G);
+        st_f32(og - i * p.dgate_stride, dg);
       }
     };
-    // the sequence that holds token t (t0 <= t <= t1): the last one that begins at or before it
-    auto seq_of = [&](int t) {
-      int n = seq;
-      while (n + 1 < p.n_seqs && __ldg(p.cu + n + 1) <= t) ++n;
-      return n;
+    auto put_first = [&](int i, const float (&uu)[V]) {
+      if (!(begins >> i & 1u) || !live || !p.dh0) return;
+      const int n = seq_of(t1 - i);
+#pragma unroll
+      for (int v = 0; v < V; ++v) p.dh0[(int64_t)n * p.C + c + v] = uu[v];
     };
-    if (first == LS) {
+    if (lim == LS && mask == 0) {
 #pragma unroll
       for (int i = 0; i < LS; ++i)
 #pragma unroll
@@ -439,8 +541,11 @@ __global__ void __launch_bounds__(kW * 32, 2) recurrence_grad_kernel(RecurrenceG
           B[v] = a[i][v] * (d[i][v] + B[v]);
           A[v] *= a[i][v];
         }
+      join<V>(sh, par, S, r, A, B, false, carry, u);
+#pragma unroll
+      for (int i = 0; i < LS; ++i) emit(i, u);
     } else {
-      int n = 0;
+      const int first = ends ? __ffs(ends) - 1 : lim;
 #pragma unroll
       for (int i = 0; i < LS; ++i) {
         if (i >= lim) continue;
@@ -453,55 +558,61 @@ __global__ void __launch_bounds__(kW * 32, 2) recurrence_grad_kernel(RecurrenceG
           continue;
         }
         if (ends >> i & 1u) {
-          n = seq_of(t1 - i);
+          const int n = seq_of(t1 - i);
 #pragma unroll
           for (int v = 0; v < V; ++v)
             B[v] = p.dh_final && live ? p.dh_final[(int64_t)n * p.C + c + v] : 0.f;
         }
-        emit(i, B, n);
+        emit(i, B);
+        put_first(i, B);
       }
-    }
-    join<V>(sh, par, S, r, A, B, ends != 0, carry, u);
-    if (first > 0) {
-      const int n = begins ? seq_of(t1) : 0;
+      join<V>(sh, par, S, r, A, B, ends != 0, carry, u);
 #pragma unroll
       for (int i = 0; i < LS; ++i)
-        if (i < first) emit(i, u, n);
+        if (i < first) {
+          emit(i, u);
+          put_first(i, u);
+        }
     }
   }
 }
 
-// How a call is spread: P runs of whole sequences (grid.y) times S CTAs of a cluster that share
-// a run's tokens, for `tiles` channel tiles.  Enough CTAs to fill the GPU twice over where the
-// tokens allow it; runs come first (they exchange nothing), as far as whole sequences can be
-// balanced, then the cluster.
+// How a call is spread: runs of whole sequences (grid.y) times S CTAs of a cluster that share a
+// run's tokens, for `tiles` channel tiles.  Two CTAs run on an SM at a time.  Runs come first
+// (they exchange nothing): about four times as many as run at once, the longest first, so that
+// the GPU's own scheduling balances them.  A cluster takes up what is left: a run longer than
+// its fair share of the tokens.
 struct Spread {
   int P, S;
   Parts parts;
+  int64_t ctas(int tiles) const { return (int64_t)tiles * P * S; }
 };
 Spread spread(const int32_t *cu, int n_seqs, int64_t T, int tiles, int chunk1) {
   Spread sp{};
   const int64_t want = std::max<int64_t>(1, 2 * device_sm_count() / std::max(1, tiles));
-  int longest = 1;
-  for (int n = 0; n < n_seqs; ++n) longest = std::max(longest, cu[n + 1] - cu[n]);
-  const int64_t pmax = std::min<int64_t>({want, T / longest, T / chunk1, kMaxParts});
-  sp.P = (int)std::max<int64_t>(1, pmax);
-  sp.parts.at[0] = 0;
-  int64_t most = 0;
-  for (int i = 1; i <= sp.P; ++i) {
-    if (i == sp.P) {
-      sp.parts.at[i] = (int32_t)T;
-    } else {
-      const int64_t goal = T * i / sp.P;
-      const int32_t *hi = std::lower_bound(cu, cu + n_seqs + 1, (int32_t)goal);
-      int32_t at = *hi;
-      if (hi != cu && goal - hi[-1] < *hi - goal) at = hi[-1];
-      sp.parts.at[i] = std::max(at, sp.parts.at[i - 1]);
-    }
-    most = std::max<int64_t>(most, sp.parts.at[i] - sp.parts.at[i - 1]);
+  const int64_t goal = std::max<int64_t>({T / (4 * want), 2 * (int64_t)chunk1, T / (kMaxParts - 1) + 1});
+  struct Run {
+    int32_t lo, hi;
+  } runs[kMaxParts];
+  int P = 0;
+  int32_t lo = 0;
+  for (int n = 1; n <= n_seqs; ++n) {
+    if (cu[n] - lo < goal && n < n_seqs) continue;
+    if (cu[n] > lo) runs[P++] = {lo, cu[n]};
+    lo = cu[n];
   }
+  if (P == 0) runs[P++] = {0, 0};
+  std::sort(runs, runs + P, [](const Run &a, const Run &b) {
+    return a.hi - a.lo != b.hi - b.lo ? a.hi - a.lo > b.hi - b.lo : a.lo < b.lo;
+  });
+  for (int i = 0; i < P; ++i) {
+    sp.parts.lo[i] = runs[i].lo;
+    sp.parts.hi[i] = runs[i].hi;
+  }
+  sp.P = P;
+  const int64_t most = runs[0].hi - runs[0].lo, fair = T / want + 1;
   sp.S = 1;
-  while (sp.S < kMaxCluster && sp.P * sp.S * 2 <= want && most > (int64_t)sp.S * chunk1) sp.S *= 2;
+  while (sp.S < kMaxCluster && 4 * most > 5 * sp.S * fair && most > (int64_t)sp.S * chunk1) sp.S *= 2;
   return sp;
 }
 
@@ -524,18 +635,40 @@ cudaError_t launch_spread(void (*kern)(Launch, Parts), const Launch &p, const Sp
   return cudaLaunchKernelEx(&cfg, kern, p, sp.parts);
 }
 
-bool vec_ok(const void *p, int64_t stride, int elem) {
-  return (reinterpret_cast<uintptr_t>(p) % (2 * elem)) == 0 && stride % 2 == 0;
+bool vec_ok(const void *p, int64_t stride, int elem, int V) {
+  return (reinterpret_cast<uintptr_t>(p) % (uintptr_t)(V * elem)) == 0 && stride % V == 0;
 }
+int tiles_of(int C, int V) { return (C + 32 * V - 1) / (32 * V); }
 
 template <typename TX, typename TG, bool LOGITS>
 cudaError_t go(const RecurrenceLaunch &p, cudaStream_t s, bool pdl) {
-  // two channels a lane where pairs are aligned; segments of as many tokens as keep the loads
-  // in flight at 16 registers an operand
-  const bool two = p.C % 2 == 0 && vec_ok(p.x, p.x_stride, sizeof(TX)) &&
-                   vec_ok(p.gate, p.gate_stride, sizeof(TG)) && vec_ok(p.y, p.y_stride, sizeof(TX));
-  constexpr int LS2 = sizeof(TX) + sizeof(TG) == 4 ? 16 : 8;
-  const int tiles = (p.C + (two ? 63 : 31)) / (two ? 64 : 32);
+  auto fits = [&](int V) {
+    return p.C % V == 0 && vec_ok(p.x, p.x_stride, sizeof(TX), V) && vec_ok(p.gate, p.gate_stride, sizeof(TG), V) &&
+           vec_ok(p.y, p.y_stride, sizeof(TX), V);
+  };
+  int longest = 0;
+  for (int n = 0; n < p.n_seqs; ++n) longest = std::max(longest, p.cu_host[n + 1] - p.cu_host[n]);
+  if (longest <= 1) {
+    const bool four = fits(4) && vec_ok(p.h0, 0, 4, 4) && vec_ok(p.h_final, 0, 4, 4);
+    const int64_t blocks = (int64_t)p.n_seqs * ((p.C + (four ? 1023 : 255)) / (four ? 1024 : 256));
+    const dim3 grid((unsigned)std::min<int64_t>(blocks, 1 << 20));
+    return four ? launch_kernel(recurrence_step_kernel<TX, TG, LOGITS, 4>, grid, dim3(256), 0, s, pdl, p)
+                : launch_kernel(recurrence_step_kernel<TX, TG, LOGITS, 1>, grid, dim3(256), 0, s, pdl, p);
+  }
+  // segments of as many tokens as keep an operand's loads in flight in 16 registers
+  constexpr bool kBoth16 = sizeof(TX) + sizeof(TG) == 4;
+  constexpr int LS2 = kBoth16 ? 16 : 8;
+  if constexpr (kBoth16) {
+    // four channels a lane take fewer instructions, where the wider tiles still fill the GPU
+    const int tiles = tiles_of(p.C, 4);
+    if (fits(4)) {
+      const Spread sp = spread(p.cu_host, p.n_seqs, p.T, tiles, kW * 8);
+      if (sp.ctas(tiles) * 2 >= 3 * device_sm_count())
+        return launch_spread<RecurrenceLaunch>(recurrence_kernel<TX, TG, LOGITS, 4, 8>, p, sp, tiles, s, pdl);
+    }
+  }
+  const bool two = fits(2);
+  const int tiles = tiles_of(p.C, two ? 2 : 1);
   const Spread sp = spread(p.cu_host, p.n_seqs, p.T, tiles, kW * (two ? LS2 : 16));
   return two ? launch_spread<RecurrenceLaunch>(recurrence_kernel<TX, TG, LOGITS, 2, LS2>, p, sp, tiles, s, pdl)
              : launch_spread<RecurrenceLaunch>(recurrence_kernel<TX, TG, LOGITS, 1, 16>, p, sp, tiles, s, pdl);
@@ -543,14 +676,14 @@ cudaError_t go(const RecurrenceLaunch &p, cudaStream_t s, bool pdl) {
 
 template <typename TX, typename TG, bool LOGITS>
 cudaError_t go(const RecurrenceGradLaunch &p, cudaStream_t s, bool pdl) {
-  const bool two = p.C % 2 == 0 && vec_ok(p.dy, p.dy_stride, sizeof(TX)) &&
-                   vec_ok(p.gate, p.gate_stride, sizeof(TG)) && vec_ok(p.y, p.y_stride, sizeof(TX)) &&
-                   vec_ok(p.dx, p.dx_stride, sizeof(TX)) && vec_ok(p.dgate, p.dgate_stride, sizeof(TG));
-  constexpr int LS2 = 8;
-  const int tiles = (p.C + (two ? 63 : 31)) / (two ? 64 : 32);
-  const Spread sp = spread(p.cu_host, p.n_seqs, p.T, tiles, kW * 8);
-  return two ? launch_spread<RecurrenceGradLaunch>(recurrence_grad_kernel<TX, TG, LOGITS, 2, LS2>, p, sp, tiles, s, pdl)
-             : launch_spread<RecurrenceGradLaunch>(recurrence_grad_kernel<TX, TG, LOGITS, 1, 8>, p, sp, tiles, s, pdl);
+  const bool two = p.C % 2 == 0 && vec_ok(p.dy, p.dy_stride, sizeof(TX), 2) &&
+                   vec_ok(p.gate, p.gate_stride, sizeof(TG), 2) && vec_ok(p.y, p.y_stride, sizeof(TX), 2) &&
+                   vec_ok(p.dx, p.dx_stride, sizeof(TX), 2) && vec_ok(p.dgate, p.dgate_stride, sizeof(TG), 2);
+  constexpr int LS = 8;
+  const int tiles = tiles_of(p.C, two ? 2 : 1);
+  const Spread sp = spread(p.cu_host, p.n_seqs, p.T, tiles, kW * LS);
+  return two ? launch_spread<RecurrenceGradLaunch>(recurrence_grad_kernel<TX, TG, LOGITS, 2, LS>, p, sp, tiles, s, pdl)
+             : launch_spread<RecurrenceGradLaunch>(recurrence_grad_kernel<TX, TG, LOGITS, 1, LS>, p, sp, tiles, s, pdl);
 }
 
 template <typename Launch>
