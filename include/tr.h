@@ -467,8 +467,9 @@ tr_status tr_projection_fp8(const uint8_t *a, int64_t a_stride, const float *a_s
  *   h0      [N, C] fp32 or NULL
  *   y       [T, C] of dtype, or NULL to keep the final states only; not x or gate
  *   h_final [N, C] fp32
- * No workspace; may be captured into a graph (a replay reads cu_seqlens again, but its spread
- * over the GPU is the captured call's: keep the same offsets).
+ * No workspace; may be captured into a graph after one uncaptured call on the device (a replay
+ * reads cu_seqlens again, but its spread over the GPU is the captured call's: keep the same
+ * offsets).
  */
 enum { TR_GATE_LOGITS = 512u };  /* tr_linear_recurrence(_backward): the gate is a logit */
 

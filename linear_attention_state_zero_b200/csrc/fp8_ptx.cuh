@@ -129,6 +129,26 @@ __device__ __forceinline__ uint32_t cluster_map(uint32_t local, uint32_t rank) {
 __device__ __forceinline__ void st_cluster(uint32_t cluster_addr, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_addr), "f"(v) : "memory");
 }
+// V floats to another CTA's shared memory, counted there as 4 V bytes of `bar`'s transaction
+// (shared::cluster addresses of one CTA).  Nothing else of this thread is waited for, as a
+// cluster barrier's release does with every global access in flight.
+__device__ __forceinline__ void st_async(uint32_t dst, const float (&f)[1], uint32_t bar) {
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(dst),
+               "r"(__float_as_uint(f[0])), "r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ void st_async(uint32_t dst, const float (&f)[2], uint32_t bar) {
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.b32 [%0], {%1, %2}, [%3];" ::"r"(dst),
+               "r"(__float_as_uint(f[0])), "r"(__float_as_uint(f[1])), "r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ void st_async(uint32_t dst, const float (&f)[4], uint32_t bar) {
+  asm volatile(
+      "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(dst),
+      "r"(__float_as_uint(f[0])), "r"(__float_as_uint(f[1])), "r"(__float_as_uint(f[2])),
+      "r"(__float_as_uint(f[3])), "r"(bar)
+      : "memory");
+}
 // Arrive on an mbarrier of any CTA of the cluster (a shared::cluster address) without ordering
 // other memory accesses: what the waiter reuses is tensor memory whose loads have completed
 // (tcgen05.wait::ld).  The release form waits for every global load in flight as well.

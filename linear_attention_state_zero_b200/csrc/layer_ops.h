@@ -72,6 +72,7 @@ struct RecurrenceLaunch {
   const float *h0;           // [N, C] or NULL
   void *y;                   // NULL: only the final states
   float *h_final;            // [N, C]
+  unsigned *err_word;
 };
 cudaError_t launch_recurrence(const RecurrenceLaunch &p, cudaStream_t s, bool pdl);
 
@@ -87,6 +88,7 @@ struct RecurrenceGradLaunch {
   const float *h0, *dh_final;   // [N, C] or NULL
   void *dx, *dgate;
   float *dh0;                   // [N, C] or NULL
+  unsigned *err_word;
 };
 cudaError_t launch_recurrence_grad(const RecurrenceGradLaunch &p, cudaStream_t s, bool pdl);
 

@@ -11,8 +11,9 @@
 // in a round each warp holds a segment of consecutive tokens of its lanes' channels in
 // registers (the next round's loads already in flight), reduces it to one map (A, B) per
 // channel, and the segments are joined in time order: the warps of a CTA through shared
-// memory, the CTAs of the cluster through each other's shared memory, one cluster barrier a
-// round.  Every warp then knows the state in front of its segment and replays the segment
+// memory, the CTAs of the cluster through each other's shared memory (stores that count their
+// bytes on the receiver's mbarrier; a cluster barrier in each round, whose release waits for
+// the loads and stores in flight, took twice as long).  Every warp then knows the state in front of its segment and replays the segment
 // from registers.  Nothing is read twice, nothing passes through global memory, and the order
 // of every sum is fixed, so results are bitwise reproducible.
 //
@@ -117,12 +118,36 @@ struct Maps {
   float start;
 };
 // The maps of a round: per warp of this CTA, and per CTA of the cluster (two sets, used in
-// turn: the barrier of a round is passed only when every reader of the round before is done).
+// turn: a CTA sends those of a round only after it has those of the round before from every
+// CTA, each of which sent them when all its warps had read the set in use now).
 template <int V>
 struct Shared {
   Maps<V> warp[2][kW];
   Maps<V> cta[2][kMaxCluster];
+  uint64_t bar[2];                 // the other CTAs' maps of a set are here
+  int abort;
 };
+
+// What a CTA starts with; with a cluster, every CTA's barriers are ready before any sends to it.
+template <int V>
+__device__ __forceinline__ void begin(Shared<V> &sh, uint32_t S) {
+  if (S == 1) return;
+  if (threadIdx.x == 0) {
+    mbar_init(smem_u32(&sh.bar[0]), 1);
+    mbar_init(smem_u32(&sh.bar[1]), 1);
+    sh.abort = 0;
+    fence_mbar_init();
+  }
+  __syncwarp();
+  cluster_sync_all();
+}
+
+// After a wait that gave up, others may still be sending: no CTA of a cluster leaves before all.
+__device__ __forceinline__ void leave(uint32_t S) {
+  if (S == 1) return;
+  __syncwarp();
+  cluster_sync_all();
+}
 
 // Where sequences begin in tokens [t0, t0 + n], n <= 31: bit i for a cu entry equal to t0 + i
 // (cu[N] = T among them); first = the last sequence with cu <= t0.  The whole warp calls it with
@@ -154,9 +179,11 @@ __device__ __forceinline__ uint32_t starts_mask(const int32_t *__restrict__ cu, 
 // Joins the maps of a round.  In: this warp's map.  Out: the value in front of this warp's
 // segment; `carry` (the value in front of the round) moves to the next round.
 template <int V>
-__device__ __forceinline__ void join(Shared<V> &sh, int par, uint32_t S, uint32_t r, const float (&A)[V],
-                                     const float (&B)[V], bool start, float (&carry)[V], float (&u)[V]) {
+__device__ __forceinline__ void join(Shared<V> &sh, int round, uint32_t S, uint32_t r, unsigned *err_word,
+                                     const float (&A)[V], const float (&B)[V], bool start, float (&carry)[V],
+                                     float (&u)[V]) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int par = round & 1;
   Maps<V> &mine = sh.warp[par][warp];
   Floats<V> fa, fb;
 #pragma unroll
@@ -207,20 +234,19 @@ __device__ __forceinline__ void join(Shared<V> &sh, int par, uint32_t S, uint32_
       ta[v] *= ma.f[v];
     }
   }
+  const uint32_t bar = smem_u32(&sh.bar[par]);
+  if (threadIdx.x == 0) mbar_arrive_expect_tx(bar, S * (256 * V + 4));
+  __syncwarp();
   if (warp < (int)S) {   // warp k tells CTA k
     Maps<V> &to = sh.cta[par][r];
-    const uint32_t da = cluster_map(smem_u32(&to.A[lane]), (uint32_t)warp);
-    const uint32_t db = cluster_map(smem_u32(&to.B[lane]), (uint32_t)warp);
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      st_cluster(da + 4 * v, ta[v]);
-      st_cluster(db + 4 * v, tb[v]);
-    }
-    if (lane == 0) st_cluster(cluster_map(smem_u32(&to.start), (uint32_t)warp), ts ? 1.f : 0.f);
+    const uint32_t k = (uint32_t)warp, there = cluster_map(bar, k);
+    st_async(cluster_map(smem_u32(&to.A[lane]), k), ta, there);
+    st_async(cluster_map(smem_u32(&to.B[lane]), k), tb, there);
+    const float flag[1] = {ts ? 1.f : 0.f};
+    if (lane == 0) st_async(cluster_map(smem_u32(&to.start), k), flag, there);
   }
-  __syncwarp();
-  cluster_arrive();
-  cluster_wait();
+  // (after a wait that gave up the rounds go on without waiting; the result is undefined)
+  mbar_wait(bar, (uint32_t)(round >> 1) & 1u, AbortFlag{&sh.abort, err_word, ERRBIT_SCAN_TIMEOUT});
 #pragma unroll
   for (uint32_t k = 0; k < kMaxCluster; ++k) {
     if (k >= S) break;
@@ -261,10 +287,7 @@ __global__ void __launch_bounds__(kW * 32, 2) recurrence_kernel(RecurrenceLaunch
   const int tb = parts.lo[blockIdx.y], te = parts.hi[blockIdx.y];
   const int chunk = (int)S * kW * LS;
   pdl_trigger();
-  if (S > 1) {   // every CTA of the cluster has started before any writes to it
-    cluster_arrive();
-    cluster_wait();
-  }
+  begin(sh, S);
   pdl_wait();
   copy_empty<V>(p.cu, p.n_seqs, (int)((blockIdx.y * S + r) * kW) + warp, (int)(gridDim.y * S * kW), c,
                 live, p.C, p.h0, p.h_final);
@@ -295,10 +318,10 @@ __global__ void __launch_bounds__(kW * 32, 2) recurrence_kernel(RecurrenceLaunch
     pg += chunk * p.gate_stride;
   };
   float carry[V] = {};
-  int par = 0, seq = 0, from = 1, to = 0;   // the sequence that was looked up last: its tokens
+  int round = 0, seq = 0, from = 1, to = 0;   // the sequence that was looked up last: its tokens
   fetch(te - t0);
 #pragma unroll 1
-  for (int tr0 = tb; tr0 < te; tr0 += chunk, t0 += chunk, py += chunk * p.y_stride, par ^= 1) {
+  for (int tr0 = tb; tr0 < te; tr0 += chunk, t0 += chunk, py += chunk * p.y_stride, ++round) {
     const int lim = te - t0 < LS ? te - t0 : LS;    // tokens of the segment (may be <= 0)
     float a[LS][V], x[LS][V];
 #pragma unroll
@@ -339,7 +362,7 @@ __global__ void __launch_bounds__(kW * 32, 2) recurrence_kernel(RecurrenceLaunch
           B[v] = fmaf(a[i][v], B[v], x[i][v]);
           A[v] *= a[i][v];
         }
-      join<V>(sh, par, S, r, A, B, false, carry, u);
+      join<V>(sh, round, S, r, p.err_word, A, B, false, carry, u);
 #pragma unroll
       for (int i = 0; i < LS; ++i) {
 #pragma unroll
@@ -373,7 +396,7 @@ __global__ void __launch_bounds__(kW * 32, 2) recurrence_kernel(RecurrenceLaunch
           if (mask >> (i + 1) & 1u) put_final(n, B);
         }
       }
-      join<V>(sh, par, S, r, A, B, inside != 0, carry, u);
+      join<V>(sh, round, S, r, p.err_word, A, B, inside != 0, carry, u);
 #pragma unroll
       for (int i = 0; i < LS; ++i) {
         if (i >= first) continue;
@@ -384,6 +407,7 @@ __global__ void __launch_bounds__(kW * 32, 2) recurrence_kernel(RecurrenceLaunch
       }
     }
   }
+  leave(S);
 }
 
 // Sequences of at most one token (decoding): h_final = a h0 + x, a thread per V channels.
@@ -425,10 +449,7 @@ __global__ void __launch_bounds__(kW * 32, 2) recurrence_grad_kernel(RecurrenceG
   const int tb = parts.lo[blockIdx.y], te = parts.hi[blockIdx.y];
   const int chunk = (int)S * kW * LS;
   pdl_trigger();
-  if (S > 1) {
-    cluster_arrive();
-    cluster_wait();
-  }
+  begin(sh, S);
   pdl_wait();
   if (p.dh0)
     copy_empty<V>(p.cu, p.n_seqs, (int)((blockIdx.y * S + r) * kW) + warp, (int)(gridDim.y * S * kW),
@@ -463,11 +484,11 @@ __global__ void __launch_bounds__(kW * 32, 2) recurrence_grad_kernel(RecurrenceG
     ph -= chunk * p.y_stride;
   };
   float carry[V] = {};
-  int par = 0, seq = 0, from = 1, to = 0;
+  int round = 0, seq = 0, from = 1, to = 0;
   fetch(t1 - tb + 1);
 #pragma unroll 1
   for (int tr1 = te - 1; tr1 >= tb;
-       tr1 -= chunk, t1 -= chunk, ox -= chunk * p.dx_stride, og -= chunk * p.dgate_stride, par ^= 1) {
+       tr1 -= chunk, t1 -= chunk, ox -= chunk * p.dx_stride, og -= chunk * p.dgate_stride, ++round) {
     const int lim = t1 - tb + 1 < LS ? t1 - tb + 1 : LS;
     // starts of the tokens [t0, t1 + 1]: token t ends its sequence when t + 1 starts one
     const int t0 = t1 - lim + 1;
@@ -541,7 +562,7 @@ __global__ void __launch_bounds__(kW * 32, 2) recurrence_grad_kernel(RecurrenceG
           B[v] = a[i][v] * (d[i][v] + B[v]);
           A[v] *= a[i][v];
         }
-      join<V>(sh, par, S, r, A, B, false, carry, u);
+      join<V>(sh, round, S, r, p.err_word, A, B, false, carry, u);
 #pragma unroll
       for (int i = 0; i < LS; ++i) emit(i, u);
     } else {
@@ -566,7 +587,7 @@ __global__ void __launch_bounds__(kW * 32, 2) recurrence_grad_kernel(RecurrenceG
         emit(i, B);
         put_first(i, B);
       }
-      join<V>(sh, par, S, r, A, B, ends != 0, carry, u);
+      join<V>(sh, round, S, r, p.err_word, A, B, ends != 0, carry, u);
 #pragma unroll
       for (int i = 0; i < LS; ++i)
         if (i < first) {
@@ -575,6 +596,7 @@ __global__ void __launch_bounds__(kW * 32, 2) recurrence_grad_kernel(RecurrenceG
         }
     }
   }
+  leave(S);
 }
 
 // How a call is spread: runs of whole sequences (grid.y) times S CTAs of a cluster that share a

@@ -1292,6 +1292,9 @@ tr_status tr_linear_recurrence(const tr_recurrence_args *a, void *stream) {
   p.h0 = a->h0;
   p.y = a->y;
   p.h_final = a->h_final;
+  int dev;
+  std::string err;
+  if (!device_state(static_cast<cudaStream_t>(stream), &dev, &p.err_word, &err)) return fail(TR_ERR_CUDA, "%s", err.c_str());
   cudaError_t e = tr::launch_recurrence(p, static_cast<cudaStream_t>(stream), true);
   if (e != cudaSuccess) return cuda_fail(e, "linear recurrence");
   return ok();
@@ -1337,6 +1340,9 @@ tr_status tr_linear_recurrence_backward(const tr_recurrence_grad_args *a, void *
   p.dx = a->dx;
   p.dgate = a->dgate;
   p.dh0 = a->dh0;
+  int dev;
+  std::string err;
+  if (!device_state(static_cast<cudaStream_t>(stream), &dev, &p.err_word, &err)) return fail(TR_ERR_CUDA, "%s", err.c_str());
   cudaError_t e = tr::launch_recurrence_grad(p, static_cast<cudaStream_t>(stream), true);
   if (e != cudaSuccess) return cuda_fail(e, "linear recurrence (backward)");
   return ok();
