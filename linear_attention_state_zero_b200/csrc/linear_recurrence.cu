@@ -85,30 +85,105 @@ __device__ __forceinline__ void st_f32(float *p, const float (&f)[V]) {
   *reinterpret_cast<Floats<V> *>(p) = r;
 }
 
+// d = a b + c, a b and a + b of V channels, two to an instruction (each rounds as the scalar one).
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+__device__ __forceinline__ void split(uint64_t d, float &lo, float &hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(d));
+}
+template <int V>
+__device__ __forceinline__ void vfma(float (&d)[V], const float (&a)[V], const float (&b)[V], const float (&c)[V]) {
+  if constexpr (V == 1) {
+    d[0] = fmaf(a[0], b[0], c[0]);
+  } else {
+#pragma unroll
+    for (int v = 0; v < V; v += 2) {
+      uint64_t r;
+      asm("fma.rn.f32x2 %0, %1, %2, %3;"
+          : "=l"(r) : "l"(pair(a[v], a[v + 1])), "l"(pair(b[v], b[v + 1])), "l"(pair(c[v], c[v + 1])));
+      split(r, d[v], d[v + 1]);
+    }
+  }
+}
+template <int V>
+__device__ __forceinline__ void vmul(float (&d)[V], const float (&a)[V], const float (&b)[V]) {
+  if constexpr (V == 1) {
+    d[0] = a[0] * b[0];
+  } else {
+#pragma unroll
+    for (int v = 0; v < V; v += 2) {
+      uint64_t r;
+      asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pair(a[v], a[v + 1])), "l"(pair(b[v], b[v + 1])));
+      split(r, d[v], d[v + 1]);
+    }
+  }
+}
+template <int V>
+__device__ __forceinline__ void vadd(float (&d)[V], const float (&a)[V], const float (&b)[V]) {
+  if constexpr (V == 1) {
+    d[0] = a[0] + b[0];
+  } else {
+#pragma unroll
+    for (int v = 0; v < V; v += 2) {
+      uint64_t r;
+      asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pair(a[v], a[v + 1])), "l"(pair(b[v], b[v + 1])));
+      split(r, d[v], d[v + 1]);
+    }
+  }
+}
+
+__device__ __forceinline__ float ex2_ftz(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 __device__ __forceinline__ float rcp_ftz(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 
-// a.  (e^gate may be infinite: a is 0 then.)
-template <bool LOGITS>
-__device__ __forceinline__ float decay(float g) {
-  return LOGITS ? rcp_ftz(1.f + exp_ftz(g)) : exp_ftz(g);
-}
-// a, and w = d(log a) / d(gate): 1, or -(1 - a) = -a e^gate for a logit.  Above 80, e^gate is held
-// at e^80 (a < 2e-35), so that the product stays finite; the minimum keeps a NaN.
-template <bool LOGITS>
-__device__ __forceinline__ float decay(float g, float &w) {
-  if (!LOGITS) {
-    w = 1.f;
-    return exp_ftz(g);
+// a, good to 2^-21: ex2 and rcp (approximate, 2^-22 each) of a rounded argument.  (e^gate may be
+// infinite: a is 0 then.)  GRAD: also q = h d(log a) / d(gate), with d(log a) / d(gate) = 1, or
+// -(1 - a) = -a e^gate for a logit; above 80, e^gate is held at e^80 there (a < 2e-35), so that
+// the product stays finite, and the minimum keeps a NaN.
+template <bool LOGITS, bool GRAD, int V>
+__device__ __forceinline__ void decay(float (&g)[V], float (&a)[V], const float (&h)[V], float (&q)[V]) {
+  float e[V], one[V], log2e[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    one[v] = 1.f;
+    log2e[v] = 1.4426950408889634f;
+    if (LOGITS && GRAD) asm("min.NaN.f32 %0, %1, %2;" : "=f"(g[v]) : "f"(g[v]), "f"(80.f));
   }
-  float c;
-  asm("min.NaN.f32 %0, %1, %2;" : "=f"(c) : "f"(g), "f"(80.f));
-  const float e = exp_ftz(c), a = rcp_ftz(1.f + e);
-  w = -e * a;
-  return a;
+  vmul(e, g, log2e);
+#pragma unroll
+  for (int v = 0; v < V; ++v) e[v] = ex2_ftz(e[v]);
+  if (!LOGITS) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      a[v] = e[v];
+      if (GRAD) q[v] = h[v];
+    }
+    return;
+  }
+  vadd(a, e, one);
+#pragma unroll
+  for (int v = 0; v < V; ++v) a[v] = rcp_ftz(a[v]);
+  if (GRAD) {
+    vmul(e, e, a);
+#pragma unroll
+    for (int v = 0; v < V; ++v) e[v] = -e[v];
+    vmul(q, e, h);
+  }
+}
+template <bool LOGITS, int V>
+__device__ __forceinline__ void decay(float (&g)[V], float (&a)[V]) {
+  float none[V] = {};
+  decay<LOGITS, false>(g, a, none, none);
 }
 
 // A map u -> A u + B per channel; `start`: a sequence begins inside, so u does not count.
@@ -200,11 +275,15 @@ __device__ __forceinline__ void join(Shared<V> &sh, int round, uint32_t S, uint3
     for (int w = 0; w < kW; ++w) {
       const Maps<V> &m = sh.warp[par][w];
       const Floats<V> ma = m.A[lane], mb = m.B[lane];
-      const bool st = any && m.start != 0.f;
+      if (w == warp) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        if (w == warp) u[v] = carry[v];
-        carry[v] = st ? mb.f[v] : fmaf(ma.f[v], carry[v], mb.f[v]);
+        for (int v = 0; v < V; ++v) u[v] = carry[v];
+      }
+      if (any && m.start != 0.f) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) carry[v] = mb.f[v];
+      } else {
+        vfma(carry, ma.f, carry, mb.f);
       }
     }
     return;
@@ -224,15 +303,20 @@ __device__ __forceinline__ void join(Shared<V> &sh, int round, uint32_t S, uint3
     const bool st = any && m.start != 0.f;
     if (w == warp) ps = ts;
     ts = ts || st;
+    if (w == warp) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      if (w == warp) {
+      for (int v = 0; v < V; ++v) {
         pa[v] = ta[v];
         pb[v] = tb[v];
       }
-      tb[v] = st ? mb.f[v] : fmaf(ma.f[v], tb[v], mb.f[v]);
-      ta[v] *= ma.f[v];
     }
+    if (st) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) tb[v] = mb.f[v];
+    } else {
+      vfma(tb, ma.f, tb, mb.f);
+    }
+    vmul(ta, ta, ma.f);
   }
   const uint32_t bar = smem_u32(&sh.bar[par]);
   if (threadIdx.x == 0) mbar_arrive_expect_tx(bar, S * (256 * V + 4));
@@ -323,14 +407,14 @@ __global__ void __launch_bounds__(kW * 32, 2) recurrence_kernel(RecurrenceLaunch
 #pragma unroll 1
   for (int tr0 = tb; tr0 < te; tr0 += chunk, t0 += chunk, py += chunk * p.y_stride, ++round) {
     const int lim = te - t0 < LS ? te - t0 : LS;    // tokens of the segment (may be <= 0)
-    float a[LS][V], x[LS][V];
+    float a[LS][V];
+    Raw<TX, V> hx[LS];   // as loaded: half the registers at two bytes, for an unpacking more
 #pragma unroll
     for (int i = 0; i < LS; ++i) {
       float g[V];
-      to_f32(nx[i], x[i]);
+      hx[i] = nx[i];
       to_f32(ng[i], g);
-#pragma unroll
-      for (int v = 0; v < V; ++v) a[i][v] = decay<LOGITS>(g[v]);
+      decay<LOGITS>(g, a[i]);
     }
     fetch(te - t0 - chunk);
     uint32_t mask = 0;
@@ -356,17 +440,18 @@ __global__ void __launch_bounds__(kW * 32, 2) recurrence_kernel(RecurrenceLaunch
     };
     if (whole) {
 #pragma unroll
-      for (int i = 0; i < LS; ++i)
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          B[v] = fmaf(a[i][v], B[v], x[i][v]);
-          A[v] *= a[i][v];
-        }
+      for (int i = 0; i < LS; ++i) {
+        float x[V];
+        to_f32(hx[i], x);
+        vfma(B, a[i], B, x);
+        vmul(A, A, a[i]);
+      }
       join<V>(sh, round, S, r, p.err_word, A, B, false, carry, u);
 #pragma unroll
       for (int i = 0; i < LS; ++i) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) u[v] = fmaf(a[i][v], u[v], x[i][v]);
+        float x[V];
+        to_f32(hx[i], x);
+        vfma(u, a[i], u, x);
         put(i, u);
       }
       if (mask >> LS) put_final(seq, u);
@@ -379,17 +464,16 @@ __global__ void __launch_bounds__(kW * 32, 2) recurrence_kernel(RecurrenceLaunch
 #pragma unroll
       for (int i = 0; i < LS; ++i) {
         if (i >= lim) continue;
+        float x[V];
+        to_f32(hx[i], x);
         if (mask >> i & 1u) {
           while (__ldg(p.cu + n + 1) <= t0 + i) ++n;
 #pragma unroll
           for (int v = 0; v < V; ++v)
-            B[v] = p.h0 && live ? fmaf(a[i][v], p.h0[(int64_t)n * p.C + c + v], x[i][v]) : x[i][v];
+            B[v] = p.h0 && live ? fmaf(a[i][v], p.h0[(int64_t)n * p.C + c + v], x[v]) : x[v];
         } else {
-#pragma unroll
-          for (int v = 0; v < V; ++v) {
-            B[v] = fmaf(a[i][v], B[v], x[i][v]);
-            A[v] *= a[i][v];
-          }
+          vfma(B, a[i], B, x);
+          vmul(A, A, a[i]);
         }
         if (i >= first) {
           put(i, B);
@@ -400,8 +484,9 @@ __global__ void __launch_bounds__(kW * 32, 2) recurrence_kernel(RecurrenceLaunch
 #pragma unroll
       for (int i = 0; i < LS; ++i) {
         if (i >= first) continue;
-#pragma unroll
-        for (int v = 0; v < V; ++v) u[v] = fmaf(a[i][v], u[v], x[i][v]);
+        float x[V];
+        to_f32(hx[i], x);
+        vfma(u, a[i], u, x);
         put(i, u);
         if (mask >> (i + 1) & 1u) put_final(seq, u);
       }
@@ -429,8 +514,9 @@ __global__ void __launch_bounds__(256) recurrence_step_kernel(RecurrenceLaunch p
       float x[V], g[V];
       to_f32(ld_raw<TX, V>(reinterpret_cast<const TX *>(p.x) + t * p.x_stride + c), x);
       to_f32(ld_raw<TG, V>(reinterpret_cast<const TG *>(p.gate) + t * p.gate_stride + c), g);
+      decay<LOGITS>(g, g);
 #pragma unroll
-      for (int v = 0; v < V; ++v) h[v] = p.h0 ? fmaf(decay<LOGITS>(g[v]), h[v], x[v]) : x[v];
+      for (int v = 0; v < V; ++v) h[v] = p.h0 ? fmaf(g[v], h[v], x[v]) : x[v];
       if (p.y) st_f32(reinterpret_cast<TX *>(p.y) + t * p.y_stride + c, h);
     }
     st_f32(p.h_final + hc, h);
@@ -520,12 +606,7 @@ __global__ void __launch_bounds__(kW * 32, 2) recurrence_grad_kernel(RecurrenceG
 #pragma unroll
         for (int v = 0; v < V; ++v) h[v] = p.h0 && live ? p.h0[(int64_t)n * p.C + c + v] : 0.f;
       }
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        float w;
-        a[i][v] = decay<LOGITS>(g[v], w);
-        q[i][v] = h[v] * w;
-      }
+      decay<LOGITS, true>(g, a[i], h, q[i]);
     }
     fetch(t1 - tb + 1 - chunk);
     float A[V], B[V], u[V];
@@ -537,12 +618,9 @@ __global__ void __launch_bounds__(kW * 32, 2) recurrence_grad_kernel(RecurrenceG
     // the token's gradients; on entry u is what reaches h_t from behind, on exit u_t
     auto emit = [&](int i, float (&uu)[V]) {
       float G[V], dg[V];
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        G[v] = d[i][v] + uu[v];
-        uu[v] = a[i][v] * G[v];
-        dg[v] = uu[v] * q[i][v];
-      }
+      vadd(G, d[i], uu);
+      vmul(uu, a[i], G);
+      vmul(dg, uu, q[i]);
       if (live) {
         st_f32(ox - i * p.dx_stride, G);
         st_f32(og - i * p.dgate_stride, dg);
@@ -556,12 +634,11 @@ __global__ void __launch_bounds__(kW * 32, 2) recurrence_grad_kernel(RecurrenceG
     };
     if (lim == LS && mask == 0) {
 #pragma unroll
-      for (int i = 0; i < LS; ++i)
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          B[v] = a[i][v] * (d[i][v] + B[v]);
-          A[v] *= a[i][v];
-        }
+      for (int i = 0; i < LS; ++i) {
+        vadd(B, d[i], B);
+        vmul(B, a[i], B);
+        vmul(A, A, a[i]);
+      }
       join<V>(sh, round, S, r, p.err_word, A, B, false, carry, u);
 #pragma unroll
       for (int i = 0; i < LS; ++i) emit(i, u);
@@ -571,11 +648,9 @@ __global__ void __launch_bounds__(kW * 32, 2) recurrence_grad_kernel(RecurrenceG
       for (int i = 0; i < LS; ++i) {
         if (i >= lim) continue;
         if (i < first) {
-#pragma unroll
-          for (int v = 0; v < V; ++v) {
-            B[v] = a[i][v] * (d[i][v] + B[v]);
-            A[v] *= a[i][v];
-          }
+          vadd(B, d[i], B);
+          vmul(B, a[i], B);
+          vmul(A, A, a[i]);
           continue;
         }
         if (ends >> i & 1u) {
