@@ -24,6 +24,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <cstddef>
 
 #include "fp8_ptx.cuh"
 #include "layer_ops.h"
@@ -33,7 +34,7 @@ namespace tr {
 namespace {
 
 constexpr int kW = 8;             // warps of a CTA: segments of a round
-constexpr int kMaxParts = 64;     // independent runs of whole sequences (grid.y)
+constexpr int kMaxParts = 128;    // independent runs of whole sequences (grid.y)
 constexpr int kMaxCluster = 8;
 
 struct Parts {
@@ -186,22 +187,85 @@ __device__ __forceinline__ void decay(float (&g)[V], float (&a)[V]) {
   decay<LOGITS, false>(g, a, none, none);
 }
 
-// A map u -> A u + B per channel; `start`: a sequence begins inside, so u does not count.
-template <int V>
-struct Maps {
-  Floats<V> A[32], B[32];
-  float start;
+// What a thread reads of one operand, V channels of LS tokens a round, a few rounds ahead: a ring
+// in shared memory that the thread alone fills and reads, by asynchronous copies, so that it
+// waits for nothing but its own copies, and the data in flight take no registers.
+template <typename T, int V, int LS>
+struct Slots {
+  static constexpr int TOKEN = kW * 32 * V * (int)sizeof(T);   // of a CTA
+  static constexpr int BYTES = LS * TOKEN;                     // a stage
+  uint8_t *mine;                                               // this thread's slot of token 0
+  __device__ explicit Slots(uint8_t *smem) : mine(smem + threadIdx.x * V * sizeof(T)) {}
+  __device__ __forceinline__ Raw<T, V> *at(int stage, int i) const {
+    return reinterpret_cast<Raw<T, V> *>(mine + stage * BYTES + i * TOKEN);
+  }
+  __device__ __forceinline__ Raw<T, V> get(int stage, int i) const { return *at(stage, i); }
 };
-// The maps of a round: per warp of this CTA, and per CTA of the cluster (two sets, used in
-// turn: a CTA sends those of a round only after it has those of the round before from every
-// CTA, each of which sent them when all its warps had read the set in use now).
+template <typename T, int V, int LS>
+struct Ring : Slots<T, V, LS> {
+  using Slots<T, V, LS>::Slots;
+  // tokens p, p + step, ... of which the first `left` exist (the others read as 0)
+  __device__ __forceinline__ void issue(int stage, const T *p, int64_t step, int left) {
+    const uint32_t dst = smem_u32(this->at(stage, 0));
+    if (left >= LS) {
+#pragma unroll
+      for (int i = 0; i < LS; ++i) copy(dst + i * this->TOKEN, p + i * step);
+    } else {
+#pragma unroll
+      for (int i = 0; i < LS; ++i)
+        if (i < left) copy(dst + i * this->TOKEN, p + i * step);
+        else *this->at(stage, i) = Raw<T, V>{};
+    }
+  }
+  static __device__ __forceinline__ void copy(uint32_t dst, const T *p) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(p), "n"(V * (int)sizeof(T)) : "memory");
+  }
+};
+// Two bytes are too few for an asynchronous copy: the loads of a stage wait in registers until
+// the next stage is issued.
+template <int LS>
+struct Ring<__nv_bfloat16, 1, LS> : Slots<__nv_bfloat16, 1, LS> {
+  Raw<__nv_bfloat16, 1> next[LS];
+  int held = -1;
+  using Slots<__nv_bfloat16, 1, LS>::Slots;
+  __device__ __forceinline__ void issue(int stage, const __nv_bfloat16 *p, int64_t step, int left) {
+    if (held >= 0) {
+#pragma unroll
+      for (int i = 0; i < LS; ++i) *this->at(held, i) = next[i];
+    }
+    held = stage;
+#pragma unroll
+    for (int i = 0; i < LS; ++i)
+      next[i] = i < left ? ld_raw<__nv_bfloat16, 1>(p + i * step) : Raw<__nv_bfloat16, 1>{};
+  }
+};
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// Rounds in the rings (the one in hand among them), for stages of `bytes`: two CTAs on an SM.
+constexpr int stages_of(int bytes) { return 65536 / bytes > 4 ? 4 : 65536 / bytes < 2 ? 2 : 65536 / bytes; }
+
+// The maps u -> A u + B of a round's segments, per channel, and the values in front of them.
+// `start`: a sequence begins inside a segment, so u does not count.  The CTAs' maps of a cluster
+// are two sets, used in turn: a CTA sends those of a round only after it has those of the round
+// before from every CTA, each of which sent them when it had read the set in use now.
 template <int V>
 struct Shared {
-  Maps<V> warp[2][kW];
-  Maps<V> cta[2][kMaxCluster];
-  uint64_t bar[2];                 // the other CTAs' maps of a set are here
+  static constexpr int C = 32 * V;
+  float A[kW][C], B[kW][C], U[kW][C];
+  float start[kW];
+  uint64_t bar[2];                 // every CTA's maps of a set are here
   int abort;
+  struct Cta {                     // (not allocated without a cluster)
+    float A[C], B[C];
+    float start;
+  } cta[2][kMaxCluster];
 };
+template <int V>
+constexpr size_t shared_bytes(int S) {
+  return S > 1 ? sizeof(Shared<V>) : offsetof(Shared<V>, cta);
+}
 
 // What a CTA starts with; with a cluster, every CTA's barriers are ready before any sends to it.
 template <int V>
@@ -252,97 +316,75 @@ __device__ __forceinline__ uint32_t starts_mask(const int32_t *__restrict__ cu, 
 }
 
 // Joins the maps of a round.  In: this warp's map.  Out: the value in front of this warp's
-// segment; `carry` (the value in front of the round) moves to the next round.
+// segment.  The first 32 V threads own a channel each: they walk the segments' maps, and keep
+// the value in front of the round (`carry`) for the next.  (Every warp walking the maps before
+// its own for its own channels took a fifth of the kernel's instructions.)
 template <int V>
 __device__ __forceinline__ void join(Shared<V> &sh, int round, uint32_t S, uint32_t r, unsigned *err_word,
-                                     const float (&A)[V], const float (&B)[V], bool start, float (&carry)[V],
+                                     const float (&A)[V], const float (&B)[V], bool start, float &carry,
                                      float (&u)[V]) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int par = round & 1;
-  Maps<V> &mine = sh.warp[par][warp];
-  Floats<V> fa, fb;
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    fa.f[v] = A[v];
-    fb.f[v] = B[v];
-  }
-  mine.A[lane] = fa;
-  mine.B[lane] = fb;
-  if (lane == 0) mine.start = start ? 1.f : 0.f;
+  st_f32(&sh.A[warp][lane * V], A);
+  st_f32(&sh.B[warp][lane * V], B);
+  if (lane == 0) sh.start[warp] = start ? 1.f : 0.f;
   const bool any = __syncthreads_or(start);
-  if (S == 1) {
+  if (threadIdx.x < 32 * V) {
+    const int ch = threadIdx.x;
+    float a[kW], b[kW];
 #pragma unroll
     for (int w = 0; w < kW; ++w) {
-      const Maps<V> &m = sh.warp[par][w];
-      const Floats<V> ma = m.A[lane], mb = m.B[lane];
-      if (w == warp) {
+      a[w] = sh.A[w][ch];
+      b[w] = sh.B[w][ch];
+    }
+    // u after a segment: one that a sequence begins in forgets what came before
+    auto after = [&](int w, float v) { return any && sh.start[w] != 0.f ? b[w] : fmaf(a[w], v, b[w]); };
+    if (S > 1) {
+      float ta[1] = {1.f}, tb[1] = {0.f};
+      bool ts = false;
 #pragma unroll
-        for (int v = 0; v < V; ++v) u[v] = carry[v];
+      for (int w = 0; w < kW; ++w) {
+        tb[0] = after(w, tb[0]);
+        ta[0] *= a[w];
+        ts = ts || (any && sh.start[w] != 0.f);
       }
-      if (any && m.start != 0.f) {
+      const int par = round & 1;
+      const uint32_t bar = smem_u32(&sh.bar[par]);
+      if (threadIdx.x == 0) mbar_arrive_expect_tx(bar, S * (256 * V + 4));
+      typename Shared<V>::Cta &to = sh.cta[par][r];
 #pragma unroll
-        for (int v = 0; v < V; ++v) carry[v] = mb.f[v];
-      } else {
-        vfma(carry, ma.f, carry, mb.f);
+      for (uint32_t k = 0; k < kMaxCluster; ++k) {
+        if (k >= S) break;
+        const uint32_t there = cluster_map(bar, k);
+        st_async(cluster_map(smem_u32(&to.A[ch]), k), ta, there);
+        st_async(cluster_map(smem_u32(&to.B[ch]), k), tb, there);
+        const float flag[1] = {ts ? 1.f : 0.f};
+        if (threadIdx.x == 0) st_async(cluster_map(smem_u32(&to.start), k), flag, there);
       }
+      // (after a wait that gave up the rounds go on without waiting; the result is undefined)
+      mbar_wait(bar, (uint32_t)(round >> 1) & 1u, AbortFlag{&sh.abort, err_word, ERRBIT_SCAN_TIMEOUT});
     }
-    return;
-  }
-  // the CTA's map up to this warp's segment (pa, pb, ps) and in all (ta, tb, ts)
-  float ta[V], tb[V], pa[V], pb[V];
-  bool ts = false, ps = false;
+    float v = carry;
+    if (S > 1) {
+      float mine = 0.f;
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    ta[v] = pa[v] = 1.f;
-    tb[v] = pb[v] = 0.f;
-  }
-#pragma unroll
-  for (int w = 0; w < kW; ++w) {
-    const Maps<V> &m = sh.warp[par][w];
-    const Floats<V> ma = m.A[lane], mb = m.B[lane];
-    const bool st = any && m.start != 0.f;
-    if (w == warp) ps = ts;
-    ts = ts || st;
-    if (w == warp) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        pa[v] = ta[v];
-        pb[v] = tb[v];
+      for (uint32_t k = 0; k < kMaxCluster; ++k) {
+        if (k >= S) break;
+        const typename Shared<V>::Cta &m = sh.cta[round & 1][k];
+        if (k == r) mine = v;
+        v = m.start != 0.f ? m.B[ch] : fmaf(m.A[ch], v, m.B[ch]);
       }
+      carry = v;
+      v = mine;
     }
-    if (st) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) tb[v] = mb.f[v];
-    } else {
-      vfma(tb, ma.f, tb, mb.f);
+    for (int w = 0; w < kW; ++w) {
+      sh.U[w][ch] = v;
+      v = after(w, v);
     }
-    vmul(ta, ta, ma.f);
+    if (S == 1) carry = v;
   }
-  const uint32_t bar = smem_u32(&sh.bar[par]);
-  if (threadIdx.x == 0) mbar_arrive_expect_tx(bar, S * (256 * V + 4));
-  __syncwarp();
-  if (warp < (int)S) {   // warp k tells CTA k
-    Maps<V> &to = sh.cta[par][r];
-    const uint32_t k = (uint32_t)warp, there = cluster_map(bar, k);
-    st_async(cluster_map(smem_u32(&to.A[lane]), k), ta, there);
-    st_async(cluster_map(smem_u32(&to.B[lane]), k), tb, there);
-    const float flag[1] = {ts ? 1.f : 0.f};
-    if (lane == 0) st_async(cluster_map(smem_u32(&to.start), k), flag, there);
-  }
-  // (after a wait that gave up the rounds go on without waiting; the result is undefined)
-  mbar_wait(bar, (uint32_t)(round >> 1) & 1u, AbortFlag{&sh.abort, err_word, ERRBIT_SCAN_TIMEOUT});
-#pragma unroll
-  for (uint32_t k = 0; k < kMaxCluster; ++k) {
-    if (k >= S) break;
-    const Maps<V> &m = sh.cta[par][k];
-    const Floats<V> ma = m.A[lane], mb = m.B[lane];
-    const bool st = m.start != 0.f;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      if (k == r) u[v] = ps ? pb[v] : fmaf(pa[v], carry[v], pb[v]);
-      carry[v] = st ? mb.f[v] : fmaf(ma.f[v], carry[v], mb.f[v]);
-    }
-  }
+  __syncthreads();
+  to_f32(ld_raw<float, V>(&sh.U[warp][lane * V]), u);
 }
 
 // Sequences without a token keep their state: to[n] = from[n] (or 0), spread over the warps
@@ -358,13 +400,17 @@ __device__ __forceinline__ void copy_empty(const int32_t *__restrict__ cu, int n
   }
 }
 
-// Registers bound it: 32 elements of a segment per thread at two bytes (16 at four) are 64 for
-// the segment in hand and 32 for the next one's loads, which with two CTAs keep 64 KB in flight
-// on each SM.
 template <typename TX, typename TG, bool LOGITS, int V, int LS>
 __global__ void __launch_bounds__(kW * 32, 2) recurrence_kernel(RecurrenceLaunch p, Parts parts) {
-  __shared__ Shared<V> sh;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  using RX = Ring<TX, V, LS>;
+  using RG = Ring<TG, V, LS>;
+  constexpr int STAGES = stages_of(RX::BYTES + RG::BYTES);
+  extern __shared__ __align__(16) uint8_t smem[];
+  RX rx(smem);
+  RG rg(smem + STAGES * RX::BYTES);
+  Shared<V> &sh = *reinterpret_cast<Shared<V> *>(smem + STAGES * (RX::BYTES + RG::BYTES));
+  // (from lane 0: the compiler then keeps token indices and row pointers in uniform registers)
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t S = cluster_size(), r = cluster_rank();
   const int c = (int)(blockIdx.x / S) * 32 * V + lane * V;
   const bool live = c < p.C;
@@ -382,41 +428,33 @@ __global__ void __launch_bounds__(kW * 32, 2) recurrence_kernel(RecurrenceLaunch
   const TX *px = reinterpret_cast<const TX *>(p.x) + (int64_t)t0 * p.x_stride + cl;
   const TG *pg = reinterpret_cast<const TG *>(p.gate) + (int64_t)t0 * p.gate_stride + cl;
   TX *py = reinterpret_cast<TX *>(p.y) + (int64_t)t0 * p.y_stride + cl;
-  Raw<TX, V> nx[LS];
-  Raw<TG, V> ng[LS];
-  auto fetch = [&](int left) {   // the segment at px, pg, of which `left` tokens exist
-    if (left >= LS) {
-#pragma unroll
-      for (int i = 0; i < LS; ++i) {
-        nx[i] = ld_raw<TX, V>(px + i * p.x_stride);
-        ng[i] = ld_raw<TG, V>(pg + i * p.gate_stride);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < LS; ++i) {
-        nx[i] = i < left ? ld_raw<TX, V>(px + i * p.x_stride) : Raw<TX, V>{};
-        ng[i] = i < left ? ld_raw<TG, V>(pg + i * p.gate_stride) : Raw<TG, V>{};
-      }
-    }
+  int ahead = te - t0;   // tokens from the next segment to fetch to the run's end
+  auto fetch = [&](int stage) {
+    rx.issue(stage, px, p.x_stride, ahead);
+    rg.issue(stage, pg, p.gate_stride, ahead);
+    cp_commit();
     px += chunk * p.x_stride;
     pg += chunk * p.gate_stride;
+    ahead -= chunk;
   };
-  float carry[V] = {};
+  float carry = 0.f;
   int round = 0, seq = 0, from = 1, to = 0;   // the sequence that was looked up last: its tokens
-  fetch(te - t0);
+  int stage = 0;
+#pragma unroll 1
+  for (int i = 0; i < STAGES - 1; ++i) fetch(i);
 #pragma unroll 1
   for (int tr0 = tb; tr0 < te; tr0 += chunk, t0 += chunk, py += chunk * p.y_stride, ++round) {
     const int lim = te - t0 < LS ? te - t0 : LS;    // tokens of the segment (may be <= 0)
-    float a[LS][V];
-    Raw<TX, V> hx[LS];   // as loaded: half the registers at two bytes, for an unpacking more
+    fetch(stage == 0 ? STAGES - 1 : stage - 1);   // into the slots of the round before
+    cp_wait<STAGES - 1>();
+    float a[LS][V], x[LS][V];
 #pragma unroll
     for (int i = 0; i < LS; ++i) {
       float g[V];
-      hx[i] = nx[i];
-      to_f32(ng[i], g);
+      to_f32(rg.get(stage, i), g);
+      to_f32(rx.get(stage, i), x[i]);
       decay<LOGITS>(g, a[i]);
     }
-    fetch(te - t0 - chunk);
     uint32_t mask = 0;
     if (lim > 0 && (t0 <= from || t0 + LS >= to)) {
       mask = starts_mask(p.cu, p.n_seqs, t0, LS, seq);
@@ -441,17 +479,13 @@ __global__ void __launch_bounds__(kW * 32, 2) recurrence_kernel(RecurrenceLaunch
     if (whole) {
 #pragma unroll
       for (int i = 0; i < LS; ++i) {
-        float x[V];
-        to_f32(hx[i], x);
-        vfma(B, a[i], B, x);
+        vfma(B, a[i], B, x[i]);
         vmul(A, A, a[i]);
       }
       join<V>(sh, round, S, r, p.err_word, A, B, false, carry, u);
 #pragma unroll
       for (int i = 0; i < LS; ++i) {
-        float x[V];
-        to_f32(hx[i], x);
-        vfma(u, a[i], u, x);
+        vfma(u, a[i], u, x[i]);
         put(i, u);
       }
       if (mask >> LS) put_final(seq, u);
@@ -464,15 +498,13 @@ __global__ void __launch_bounds__(kW * 32, 2) recurrence_kernel(RecurrenceLaunch
 #pragma unroll
       for (int i = 0; i < LS; ++i) {
         if (i >= lim) continue;
-        float x[V];
-        to_f32(hx[i], x);
         if (mask >> i & 1u) {
           while (__ldg(p.cu + n + 1) <= t0 + i) ++n;
 #pragma unroll
           for (int v = 0; v < V; ++v)
-            B[v] = p.h0 && live ? fmaf(a[i][v], p.h0[(int64_t)n * p.C + c + v], x[v]) : x[v];
+            B[v] = p.h0 && live ? fmaf(a[i][v], p.h0[(int64_t)n * p.C + c + v], x[i][v]) : x[i][v];
         } else {
-          vfma(B, a[i], B, x);
+          vfma(B, a[i], B, x[i]);
           vmul(A, A, a[i]);
         }
         if (i >= first) {
@@ -484,13 +516,12 @@ __global__ void __launch_bounds__(kW * 32, 2) recurrence_kernel(RecurrenceLaunch
 #pragma unroll
       for (int i = 0; i < LS; ++i) {
         if (i >= first) continue;
-        float x[V];
-        to_f32(hx[i], x);
-        vfma(u, a[i], u, x);
+        vfma(u, a[i], u, x[i]);
         put(i, u);
         if (mask >> (i + 1) & 1u) put_final(seq, u);
       }
     }
+    stage = stage == STAGES - 1 ? 0 : stage + 1;
   }
   leave(S);
 }
@@ -527,8 +558,15 @@ __global__ void __launch_bounds__(256) recurrence_step_kernel(RecurrenceLaunch p
 // sequence "begins" at its last token.
 template <typename TX, typename TG, bool LOGITS, int V, int LS>
 __global__ void __launch_bounds__(kW * 32, 2) recurrence_grad_kernel(RecurrenceGradLaunch p, Parts parts) {
-  __shared__ Shared<V> sh;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  using RX = Ring<TX, V, LS>;
+  using RG = Ring<TG, V, LS>;
+  constexpr int STAGES = stages_of(2 * RX::BYTES + RG::BYTES);
+  extern __shared__ __align__(16) uint8_t smem[];
+  RX rd(smem), rh(smem + STAGES * RX::BYTES);
+  RG rg(smem + 2 * STAGES * RX::BYTES);
+  Shared<V> &sh = *reinterpret_cast<Shared<V> *>(smem + STAGES * (2 * RX::BYTES + RG::BYTES));
+  // (from lane 0: the compiler then keeps token indices and row pointers in uniform registers)
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t S = cluster_size(), r = cluster_rank();
   const int c = (int)(blockIdx.x / S) * 32 * V + lane * V;
   const bool live = c < p.C;
@@ -547,31 +585,22 @@ __global__ void __launch_bounds__(kW * 32, 2) recurrence_grad_kernel(RecurrenceG
   const TX *ph = reinterpret_cast<const TX *>(p.y) + (int64_t)(t1 - 1) * p.y_stride + cl;   // h_{t-1}
   TX *ox = reinterpret_cast<TX *>(p.dx) + (int64_t)t1 * p.dx_stride + cl;
   TG *og = reinterpret_cast<TG *>(p.dgate) + (int64_t)t1 * p.dgate_stride + cl;
-  Raw<TX, V> nd[LS], nh[LS];
-  Raw<TG, V> ng[LS];
-  auto fetch = [&](int left) {
-    if (left > LS) {
-#pragma unroll
-      for (int i = 0; i < LS; ++i) {
-        nd[i] = ld_raw<TX, V>(pd - i * p.dy_stride);
-        ng[i] = ld_raw<TG, V>(pg - i * p.gate_stride);
-        nh[i] = ld_raw<TX, V>(ph - i * p.y_stride);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < LS; ++i) {
-        nd[i] = i < left ? ld_raw<TX, V>(pd - i * p.dy_stride) : Raw<TX, V>{};
-        ng[i] = i < left ? ld_raw<TG, V>(pg - i * p.gate_stride) : Raw<TG, V>{};
-        nh[i] = i < left - 1 ? ld_raw<TX, V>(ph - i * p.y_stride) : Raw<TX, V>{};
-      }
-    }
+  int ahead = t1 - tb + 1;   // tokens from the run's begin to the next segment to fetch
+  auto fetch = [&](int stage) {
+    rd.issue(stage, pd, -p.dy_stride, ahead);
+    rh.issue(stage, ph, -p.y_stride, ahead - 1);
+    rg.issue(stage, pg, -p.gate_stride, ahead);
+    cp_commit();
     pd -= chunk * p.dy_stride;
-    pg -= chunk * p.gate_stride;
     ph -= chunk * p.y_stride;
+    pg -= chunk * p.gate_stride;
+    ahead -= chunk;
   };
-  float carry[V] = {};
+  float carry = 0.f;
   int round = 0, seq = 0, from = 1, to = 0;
-  fetch(t1 - tb + 1);
+  int stage = 0;
+#pragma unroll 1
+  for (int i = 0; i < STAGES - 1; ++i) fetch(i);
 #pragma unroll 1
   for (int tr1 = te - 1; tr1 >= tb;
        tr1 -= chunk, t1 -= chunk, ox -= chunk * p.dx_stride, og -= chunk * p.dgate_stride, ++round) {
@@ -594,13 +623,15 @@ __global__ void __launch_bounds__(kW * 32, 2) recurrence_grad_kernel(RecurrenceG
     const uint32_t rev = lim > 0 ? __brev(mask) >> (31 - lim) : 0u;  // bit j: t0 + lim - j starts
     const uint32_t ends = rev & ((1u << (lim > 0 ? lim : 0)) - 1u);
     const uint32_t begins = rev >> 1;
+    fetch(stage == 0 ? STAGES - 1 : stage - 1);   // into the slots of the round before
+    cp_wait<STAGES - 1>();
     float a[LS][V], d[LS][V], q[LS][V];   // q = h_{t-1} d(log a)/d(gate)
 #pragma unroll
     for (int i = 0; i < LS; ++i) {
       float g[V], h[V];
-      to_f32(nd[i], d[i]);
-      to_f32(nh[i], h);
-      to_f32(ng[i], g);
+      to_f32(rd.get(stage, i), d[i]);
+      to_f32(rh.get(stage, i), h);
+      to_f32(rg.get(stage, i), g);
       if (begins >> i & 1u) {
         const int n = seq_of(t1 - i);
 #pragma unroll
@@ -608,7 +639,6 @@ __global__ void __launch_bounds__(kW * 32, 2) recurrence_grad_kernel(RecurrenceG
       }
       decay<LOGITS, true>(g, a[i], h, q[i]);
     }
-    fetch(t1 - tb + 1 - chunk);
     float A[V], B[V], u[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -670,13 +700,14 @@ __global__ void __launch_bounds__(kW * 32, 2) recurrence_grad_kernel(RecurrenceG
           put_first(i, u);
         }
     }
+    stage = stage == STAGES - 1 ? 0 : stage + 1;
   }
   leave(S);
 }
 
 // How a call is spread: runs of whole sequences (grid.y) times S CTAs of a cluster that share a
 // run's tokens, for `tiles` channel tiles.  Two CTAs run on an SM at a time.  Runs come first
-// (they exchange nothing): about four times as many as run at once, the longest first, so that
+// (they exchange nothing): up to eight times as many as run at once, the longest first, so that
 // the GPU's own scheduling balances them.  A cluster takes up what is left: a run longer than
 // its fair share of the tokens.
 struct Spread {
@@ -687,7 +718,7 @@ struct Spread {
 Spread spread(const int32_t *cu, int n_seqs, int64_t T, int tiles, int chunk1) {
   Spread sp{};
   const int64_t want = std::max<int64_t>(1, 2 * device_sm_count() / std::max(1, tiles));
-  const int64_t goal = std::max<int64_t>({T / (4 * want), 2 * (int64_t)chunk1, T / (kMaxParts - 1) + 1});
+  const int64_t goal = std::max<int64_t>({T / (8 * want), 2 * (int64_t)chunk1, T / (kMaxParts - 1) + 1});
   struct Run {
     int32_t lo, hi;
   } runs[kMaxParts];
@@ -713,9 +744,13 @@ Spread spread(const int32_t *cu, int n_seqs, int64_t T, int tiles, int chunk1) {
   return sp;
 }
 
-template <typename Launch>
-cudaError_t launch_spread(void (*kern)(Launch, Parts), const Launch &p, const Spread &sp, int tiles,
+// `stage`: bytes of a round's operands in a CTA
+template <int V, typename Launch>
+cudaError_t launch_spread(void (*kern)(Launch, Parts), const Launch &p, const Spread &sp, int tiles, int stage,
                           cudaStream_t s, bool pdl) {
+  const size_t smem = (size_t)stages_of(stage) * stage + shared_bytes<V>(sp.S);
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = (unsigned)sp.S;
@@ -726,6 +761,7 @@ cudaError_t launch_spread(void (*kern)(Launch, Parts), const Launch &p, const Sp
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(tiles * sp.S), (unsigned)sp.P);
   cfg.blockDim = dim3(kW * 32);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = pdl ? 2 : 1;
@@ -752,23 +788,25 @@ cudaError_t go(const RecurrenceLaunch &p, cudaStream_t s, bool pdl) {
     return four ? launch_kernel(recurrence_step_kernel<TX, TG, LOGITS, 4>, grid, dim3(256), 0, s, pdl, p)
                 : launch_kernel(recurrence_step_kernel<TX, TG, LOGITS, 1>, grid, dim3(256), 0, s, pdl, p);
   }
-  // segments of as many tokens as keep an operand's loads in flight in 16 registers
-  constexpr bool kBoth16 = sizeof(TX) + sizeof(TG) == 4;
+  // segments of 32 elements a thread where both operands have two bytes, else of 16
+  constexpr int kTok = sizeof(TX) + sizeof(TG);
+  constexpr bool kBoth16 = kTok == 4;
   constexpr int LS2 = kBoth16 ? 16 : 8;
   if constexpr (kBoth16) {
-    // four channels a lane take fewer instructions, where the wider tiles still fill the GPU
+    // four channels a lane take fewer instructions, where the wider tiles still fill the GPU (and
+    // need no cluster, whose maps would leave room for one CTA on an SM only)
     const int tiles = tiles_of(p.C, 4);
     if (fits(4)) {
       const Spread sp = spread(p.cu_host, p.n_seqs, p.T, tiles, kW * 8);
-      if (sp.ctas(tiles) * 2 >= 3 * device_sm_count())
-        return launch_spread<RecurrenceLaunch>(recurrence_kernel<TX, TG, LOGITS, 4, 8>, p, sp, tiles, s, pdl);
+      if (sp.S == 1 && sp.ctas(tiles) * 2 >= 3 * device_sm_count())
+        return launch_spread<4>(recurrence_kernel<TX, TG, LOGITS, 4, 8>, p, sp, tiles, kW * 32 * 4 * 8 * kTok, s, pdl);
     }
   }
   const bool two = fits(2);
   const int tiles = tiles_of(p.C, two ? 2 : 1);
   const Spread sp = spread(p.cu_host, p.n_seqs, p.T, tiles, kW * (two ? LS2 : 16));
-  return two ? launch_spread<RecurrenceLaunch>(recurrence_kernel<TX, TG, LOGITS, 2, LS2>, p, sp, tiles, s, pdl)
-             : launch_spread<RecurrenceLaunch>(recurrence_kernel<TX, TG, LOGITS, 1, 16>, p, sp, tiles, s, pdl);
+  return two ? launch_spread<2>(recurrence_kernel<TX, TG, LOGITS, 2, LS2>, p, sp, tiles, kW * 32 * 2 * LS2 * kTok, s, pdl)
+             : launch_spread<1>(recurrence_kernel<TX, TG, LOGITS, 1, 16>, p, sp, tiles, kW * 32 * 16 * kTok, s, pdl);
 }
 
 template <typename TX, typename TG, bool LOGITS>
@@ -779,8 +817,9 @@ cudaError_t go(const RecurrenceGradLaunch &p, cudaStream_t s, bool pdl) {
   constexpr int LS = 8;
   const int tiles = tiles_of(p.C, two ? 2 : 1);
   const Spread sp = spread(p.cu_host, p.n_seqs, p.T, tiles, kW * LS);
-  return two ? launch_spread<RecurrenceGradLaunch>(recurrence_grad_kernel<TX, TG, LOGITS, 2, LS>, p, sp, tiles, s, pdl)
-             : launch_spread<RecurrenceGradLaunch>(recurrence_grad_kernel<TX, TG, LOGITS, 1, LS>, p, sp, tiles, s, pdl);
+  constexpr int kTok = 2 * sizeof(TX) + sizeof(TG);
+  return two ? launch_spread<2>(recurrence_grad_kernel<TX, TG, LOGITS, 2, LS>, p, sp, tiles, kW * 32 * 2 * LS * kTok, s, pdl)
+             : launch_spread<1>(recurrence_grad_kernel<TX, TG, LOGITS, 1, LS>, p, sp, tiles, kW * 32 * LS * kTok, s, pdl);
 }
 
 template <typename Launch>
