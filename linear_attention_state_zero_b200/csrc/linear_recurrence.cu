@@ -34,11 +34,13 @@ namespace tr {
 namespace {
 
 constexpr int kW = 8;             // warps of a CTA: segments of a round
-constexpr int kMaxParts = 128;    // independent runs of whole sequences (grid.y)
+constexpr int kMaxParts = 64;     // independent runs of whole sequences (grid.y)
 constexpr int kMaxCluster = 8;
 
 struct Parts {
-  int32_t lo[kMaxParts], hi[kMaxParts];   // tokens of each run, the longest first
+  int32_t lo[kMaxParts], hi[kMaxParts];           // tokens of each run, the longest first
+  int32_t seq_lo[kMaxParts], seq_hi[kMaxParts];   // its sequences: cu[seq_lo] = lo, cu[seq_hi] = hi
+  int some_empty;                                 // some sequence has no token
 };
 
 template <int V> struct alignas(4 * V) Floats { float f[V]; };
@@ -288,31 +290,54 @@ __device__ __forceinline__ void leave(uint32_t S) {
   cluster_sync_all();
 }
 
-// Where sequences begin in tokens [t0, t0 + n], n <= 31: bit i for a cu entry equal to t0 + i
-// (cu[N] = T among them); first = the last sequence with cu <= t0.  The whole warp calls it with
-// the same arguments.
-__device__ __forceinline__ uint32_t starts_mask(const int32_t *__restrict__ cu, int n_seqs, int t0,
-                                                int n, int &first) {
+// The sequence that holds token t0 (the last with cu <= t0: seq, its tokens from .. to - 1), and
+// where sequences begin in the tokens [t0, t0 + n], n < 31: bit i for a cu entry equal to t0 + i
+// (cu[N] = T among them).  lookup_up starts from a sequence `seq` that begins at or before t0,
+// lookup_down from an entry `top` that is past t0 + n or the last such (and cu[low] <= t0).  The
+// whole warp calls them with the same arguments; one load of 32 entries is the rule.
+__device__ __forceinline__ uint32_t bits_of(int v, int t0, int n) {
+  return v >= t0 && v - t0 <= n ? 1u << (v - t0) : 0u;
+}
+__device__ __forceinline__ uint32_t lookup_up(const int32_t *__restrict__ cu, int n_seqs, int t0, int n, int &seq,
+                                              int &from, int &to) {
   const int lane = threadIdx.x & 31;
-  // the last index in [0, n_seqs] with cu <= t0, 32 probes a step
-  int lo = 0, hi = n_seqs + 1;                // cu[lo] <= t0, cu[hi] > t0 (hi: past the end)
-  while (hi - lo > 1) {
-    const int step = (hi - lo + 31) / 32;
-    const int at = lo + (lane + 1) * step;    // lane 31 is at or past hi
-    const bool le = at < hi && __ldg(cu + at) <= t0;
-    const int k = __popc(__ballot_sync(0xffffffffu, le));   // probes that hold are a prefix
-    const int nlo = lo + k * step;
-    hi = nlo + step < hi ? nlo + step : hi;
-    lo = nlo;
+  int at = seq, v;
+  uint32_t le;
+  for (;; at += 31) {
+    v = __ldg(cu + (at + lane < n_seqs ? at + lane : n_seqs));
+    le = __ballot_sync(0xffffffffu, v <= t0);   // lanes 0 .. k
+    if (le != 0xffffffffu) break;
   }
-  first = lo;
-  uint32_t m = __ldg(cu + lo) == t0 ? 1u : 0u;
-  for (int i = lo + 1 + lane;; i += 32) {
-    const bool past = i > n_seqs || __ldg(cu + i) - t0 > n;
-    if (!past) m |= 1u << (__ldg(cu + i) - t0);
-    if (__ballot_sync(0xffffffffu, past)) break;
+  const int k = __popc(le) - 1;
+  seq = at + k;
+  from = __shfl_sync(0xffffffffu, v, k);
+  to = __shfl_sync(0xffffffffu, v, k + 1);
+  uint32_t m = bits_of(v, t0, n);
+  while (__shfl_sync(0xffffffffu, v, 31) <= t0 + n && at + 31 < n_seqs) {
+    at += 31;
+    v = __ldg(cu + (at + lane < n_seqs ? at + lane : n_seqs));
+    m |= bits_of(v, t0, n);
   }
   return __reduce_or_sync(0xffffffffu, m);
+}
+__device__ __forceinline__ uint32_t lookup_down(const int32_t *__restrict__ cu, int low, int top, int t0, int n,
+                                                int &seq, int &from, int &to) {
+  const int lane = threadIdx.x & 31;
+  uint32_t m = 0;
+  for (;;) {
+    const int at = top - 31 > low ? top - 31 : low;
+    const int v = __ldg(cu + (at + lane < top ? at + lane : top));
+    m |= bits_of(v, t0, n);
+    const uint32_t le = __ballot_sync(0xffffffffu, v <= t0);
+    if (le) {
+      const int k = __popc(le) - 1;
+      seq = at + k;
+      from = __shfl_sync(0xffffffffu, v, k);
+      to = __shfl_sync(0xffffffffu, v, k + 1);
+      return __reduce_or_sync(0xffffffffu, m);
+    }
+    top = at;
+  }
 }
 
 // Joins the maps of a round.  In: this warp's map.  Out: the value in front of this warp's
@@ -419,8 +444,6 @@ __global__ void __launch_bounds__(kW * 32, 2) recurrence_kernel(RecurrenceLaunch
   pdl_trigger();
   begin(sh, S);
   pdl_wait();
-  copy_empty<V>(p.cu, p.n_seqs, (int)((blockIdx.y * S + r) * kW) + warp, (int)(gridDim.y * S * kW), c,
-                live, p.C, p.h0, p.h_final);
   // lanes past the last channel load the last ones and store nothing
   const int cl = live ? c : p.C - V;
   const bool put_y = live && p.y;
@@ -438,10 +461,13 @@ __global__ void __launch_bounds__(kW * 32, 2) recurrence_kernel(RecurrenceLaunch
     ahead -= chunk;
   };
   float carry = 0.f;
-  int round = 0, seq = 0, from = 1, to = 0;   // the sequence that was looked up last: its tokens
-  int stage = 0;
+  int round = 0, stage = 0;
+  int seq = parts.seq_lo[blockIdx.y], from = te, to = 0;   // the sequence looked up last: its tokens
 #pragma unroll 1
   for (int i = 0; i < STAGES - 1; ++i) fetch(i);
+  if (parts.some_empty)
+    copy_empty<V>(p.cu, p.n_seqs, (int)((blockIdx.y * S + r) * kW) + warp, (int)(gridDim.y * S * kW), c,
+                  live, p.C, p.h0, p.h_final);
 #pragma unroll 1
   for (int tr0 = tb; tr0 < te; tr0 += chunk, t0 += chunk, py += chunk * p.y_stride, ++round) {
     const int lim = te - t0 < LS ? te - t0 : LS;    // tokens of the segment (may be <= 0)
@@ -456,11 +482,7 @@ __global__ void __launch_bounds__(kW * 32, 2) recurrence_kernel(RecurrenceLaunch
       decay<LOGITS>(g, a[i]);
     }
     uint32_t mask = 0;
-    if (lim > 0 && (t0 <= from || t0 + LS >= to)) {
-      mask = starts_mask(p.cu, p.n_seqs, t0, LS, seq);
-      from = __ldg(p.cu + seq);
-      to = __ldg(p.cu + seq + 1);
-    }
+    if (lim > 0 && (t0 <= from || t0 + LS >= to)) mask = lookup_up(p.cu, p.n_seqs, t0, LS, seq, from, to);
     const bool whole = lim == LS && (mask & ~(1u << LS)) == 0;   // of one sequence, begun before
     float A[V], B[V], u[V];
 #pragma unroll
@@ -575,9 +597,6 @@ __global__ void __launch_bounds__(kW * 32, 2) recurrence_grad_kernel(RecurrenceG
   pdl_trigger();
   begin(sh, S);
   pdl_wait();
-  if (p.dh0)
-    copy_empty<V>(p.cu, p.n_seqs, (int)((blockIdx.y * S + r) * kW) + warp, (int)(gridDim.y * S * kW),
-                  c, live, p.C, p.dh_final, p.dh0);
   const int cl = live ? c : p.C - V;
   int t1 = te - 1 - ((int)r * kW * LS + warp * LS);
   const TX *pd = reinterpret_cast<const TX *>(p.dy) + (int64_t)t1 * p.dy_stride + cl;
@@ -597,10 +616,14 @@ __global__ void __launch_bounds__(kW * 32, 2) recurrence_grad_kernel(RecurrenceG
     ahead -= chunk;
   };
   float carry = 0.f;
-  int round = 0, seq = 0, from = 1, to = 0;
-  int stage = 0;
+  int round = 0, stage = 0;
+  const int low = parts.seq_lo[blockIdx.y];
+  int seq = parts.seq_hi[blockIdx.y] - 1, from = te, to = 0;   // the sequence looked up last
 #pragma unroll 1
   for (int i = 0; i < STAGES - 1; ++i) fetch(i);
+  if (parts.some_empty && p.dh0)
+    copy_empty<V>(p.cu, p.n_seqs, (int)((blockIdx.y * S + r) * kW) + warp, (int)(gridDim.y * S * kW),
+                  c, live, p.C, p.dh_final, p.dh0);
 #pragma unroll 1
   for (int tr1 = te - 1; tr1 >= tb;
        tr1 -= chunk, t1 -= chunk, ox -= chunk * p.dx_stride, og -= chunk * p.dgate_stride, ++round) {
@@ -608,11 +631,8 @@ __global__ void __launch_bounds__(kW * 32, 2) recurrence_grad_kernel(RecurrenceG
     // starts of the tokens [t0, t1 + 1]: token t ends its sequence when t + 1 starts one
     const int t0 = t1 - lim + 1;
     uint32_t mask = 0;
-    if (lim > 0 && (t0 <= from || t1 + 1 >= to)) {
-      mask = starts_mask(p.cu, p.n_seqs, t0, lim, seq);
-      from = __ldg(p.cu + seq);
-      to = __ldg(p.cu + seq + 1);
-    }
+    if (lim > 0 && (t0 <= from || t1 + 1 >= to))
+      mask = lookup_down(p.cu, low, seq + 1, t0, lim, seq, from, to);
     // the sequence that holds token t (t0 <= t <= t1): the last one that begins at or before it
     auto seq_of = [&](int t) {
       int n = seq;
@@ -720,22 +740,24 @@ Spread spread(const int32_t *cu, int n_seqs, int64_t T, int tiles, int chunk1) {
   const int64_t want = std::max<int64_t>(1, 2 * device_sm_count() / std::max(1, tiles));
   const int64_t goal = std::max<int64_t>({T / (8 * want), 2 * (int64_t)chunk1, T / (kMaxParts - 1) + 1});
   struct Run {
-    int32_t lo, hi;
+    int32_t lo, hi, seq_lo, seq_hi;
   } runs[kMaxParts];
-  int P = 0;
-  int32_t lo = 0;
+  int P = 0, first = 0;
   for (int n = 1; n <= n_seqs; ++n) {
-    if (cu[n] - lo < goal && n < n_seqs) continue;
-    if (cu[n] > lo) runs[P++] = {lo, cu[n]};
-    lo = cu[n];
+    sp.parts.some_empty |= cu[n] == cu[n - 1];
+    if (cu[n] - cu[first] < goal && n < n_seqs) continue;
+    if (cu[n] > cu[first]) runs[P++] = {cu[first], cu[n], first, n};
+    first = n;
   }
-  if (P == 0) runs[P++] = {0, 0};
+  if (P == 0) runs[P++] = {0, 0, 0, 0};
   std::sort(runs, runs + P, [](const Run &a, const Run &b) {
     return a.hi - a.lo != b.hi - b.lo ? a.hi - a.lo > b.hi - b.lo : a.lo < b.lo;
   });
   for (int i = 0; i < P; ++i) {
     sp.parts.lo[i] = runs[i].lo;
     sp.parts.hi[i] = runs[i].hi;
+    sp.parts.seq_lo[i] = runs[i].seq_lo;
+    sp.parts.seq_hi[i] = runs[i].seq_hi;
   }
   sp.P = P;
   const int64_t most = runs[0].hi - runs[0].lo, fair = T / want + 1;
