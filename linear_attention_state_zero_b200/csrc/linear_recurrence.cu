@@ -8,12 +8,12 @@
 // -(1 - a) d(log a)).  Both are one scan of maps u -> A u + B, in time and against it.
 //
 // One pass over HBM: a cluster of up to 8 CTAs owns a tile of channels and walks the tokens;
-// in a round each warp holds a segment of consecutive tokens of its lanes' channels in
-// registers (the next round's loads already in flight), reduces it to one map (A, B) per
-// channel, and the segments are joined in time order: the warps of a CTA through shared
-// memory, the CTAs of the cluster through each other's shared memory (stores that count their
+// in a round each warp (or each of G groups of its lanes) holds a segment of consecutive tokens
+// of its lanes' channels in registers (the next rounds' loads already in flight), reduces it to
+// one map (A, B) per channel, and the segments are joined in time order: those of a CTA through
+// shared memory, the CTAs of the cluster through each other's shared memory (stores that count their
 // bytes on the receiver's mbarrier; a cluster barrier in each round, whose release waits for
-// the loads and stores in flight, took twice as long).  Every warp then knows the state in front of its segment and replays the segment
+// the loads and stores in flight, took twice as long).  Every lane then knows the state in front of its segment and replays the segment
 // from registers.  Nothing is read twice, nothing passes through global memory, and the order
 // of every sum is fixed, so results are bitwise reproducible.
 //
@@ -33,7 +33,7 @@
 namespace tr {
 namespace {
 
-constexpr int kW = 8;             // warps of a CTA: segments of a round
+constexpr int kW = 8;             // warps of a CTA
 constexpr int kMaxParts = 64;     // independent runs of whole sequences (grid.y)
 constexpr int kMaxCluster = 8;
 
@@ -220,7 +220,11 @@ struct Ring : Slots<T, V, LS> {
     }
   }
   static __device__ __forceinline__ void copy(uint32_t dst, const T *p) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(p), "n"(V * (int)sizeof(T)) : "memory");
+    if constexpr (V * sizeof(T) == 16) {   // (past the L1 cache, which smaller copies go through)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(p) : "memory");
+    } else {
+      asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(p), "n"(V * (int)sizeof(T)) : "memory");
+    }
   }
 };
 // Two bytes are too few for an asynchronous copy: the loads of a stage wait in registers until
@@ -252,11 +256,11 @@ constexpr int stages_of(int bytes) { return 65536 / bytes > 4 ? 4 : 65536 / byte
 // `start`: a sequence begins inside a segment, so u does not count.  The CTAs' maps of a cluster
 // are two sets, used in turn: a CTA sends those of a round only after it has those of the round
 // before from every CTA, each of which sent them when it had read the set in use now.
-template <int V>
+template <int V, int G>
 struct Shared {
-  static constexpr int C = 32 * V;
-  float A[kW][C], B[kW][C], U[kW][C];
-  float start[kW];
+  static constexpr int C = 32 / G * V, SEGS = kW * G;
+  float A[SEGS][C], B[SEGS][C], U[SEGS][C];
+  float start[SEGS];
   uint64_t bar[2];                 // every CTA's maps of a set are here
   int abort;
   struct Cta {                     // (not allocated without a cluster)
@@ -264,14 +268,15 @@ struct Shared {
     float start;
   } cta[2][kMaxCluster];
 };
-template <int V>
-constexpr size_t shared_bytes(int S) {
-  return S > 1 ? sizeof(Shared<V>) : offsetof(Shared<V>, cta);
+template <int V, int G>
+size_t shared_bytes(int S) {
+  typedef Shared<V, G> Sh;
+  return S > 1 ? sizeof(Sh) : offsetof(Sh, cta);
 }
 
 // What a CTA starts with; with a cluster, every CTA's barriers are ready before any sends to it.
-template <int V>
-__device__ __forceinline__ void begin(Shared<V> &sh, uint32_t S) {
+template <int V, int G>
+__device__ __forceinline__ void begin(Shared<V, G> &sh, uint32_t S) {
   if (S == 1) return;
   if (threadIdx.x == 0) {
     mbar_init(smem_u32(&sh.bar[0]), 1);
@@ -340,61 +345,55 @@ __device__ __forceinline__ uint32_t lookup_down(const int32_t *__restrict__ cu, 
   }
 }
 
-// Joins the maps of a round.  In: this warp's map.  Out: the value in front of this warp's
-// segment.  The first 32 V threads own a channel each: they walk the segments' maps, and keep
-// the value in front of the round (`carry`) for the next.  (Every warp walking the maps before
-// its own for its own channels took a fifth of the kernel's instructions.)
-template <int V>
-__device__ __forceinline__ void join(Shared<V> &sh, int round, uint32_t S, uint32_t r, unsigned *err_word,
-                                     const float (&A)[V], const float (&B)[V], bool start, float &carry,
+// Joins the maps of a round.  In: the map of this lane's segment.  Out: the value in front of
+// it.  The first 32 V / G threads own a channel each: they walk the segments' maps, and keep the
+// value in front of the round (`carry`) for the next.  (Every warp walking the maps before its
+// own for its own channels took a fifth of the kernel's instructions.)
+template <int V, int G>
+__device__ __forceinline__ void join(Shared<V, G> &sh, int round, uint32_t S, uint32_t r, unsigned *err_word, int seg,
+                                     int li, const float (&A)[V], const float (&B)[V], bool start, float &carry,
                                      float (&u)[V]) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  st_f32(&sh.A[warp][lane * V], A);
-  st_f32(&sh.B[warp][lane * V], B);
-  if (lane == 0) sh.start[warp] = start ? 1.f : 0.f;
+  typedef Shared<V, G> Sh;
+  __syncwarp();
+  st_f32(&sh.A[seg][li * V], A);
+  st_f32(&sh.B[seg][li * V], B);
+  if (li == 0) sh.start[seg] = start ? 1.f : 0.f;
   const bool any = __syncthreads_or(start);
-  if (threadIdx.x < 32 * V) {
+  if (threadIdx.x < Sh::C) {
     const int ch = threadIdx.x;
-    float a[kW], b[kW];
-#pragma unroll
-    for (int w = 0; w < kW; ++w) {
-      a[w] = sh.A[w][ch];
-      b[w] = sh.B[w][ch];
-    }
     // u after a segment: one that a sequence begins in forgets what came before
-    auto after = [&](int w, float v) { return any && sh.start[w] != 0.f ? b[w] : fmaf(a[w], v, b[w]); };
+    auto after = [&](int w, float v) {
+      return any && sh.start[w] != 0.f ? sh.B[w][ch] : fmaf(sh.A[w][ch], v, sh.B[w][ch]);
+    };
+    float v = carry;
     if (S > 1) {
       float ta[1] = {1.f}, tb[1] = {0.f};
       bool ts = false;
 #pragma unroll
-      for (int w = 0; w < kW; ++w) {
+      for (int w = 0; w < Sh::SEGS; ++w) {
         tb[0] = after(w, tb[0]);
-        ta[0] *= a[w];
+        ta[0] *= sh.A[w][ch];
         ts = ts || (any && sh.start[w] != 0.f);
       }
       const int par = round & 1;
       const uint32_t bar = smem_u32(&sh.bar[par]);
-      if (threadIdx.x == 0) mbar_arrive_expect_tx(bar, S * (256 * V + 4));
-      typename Shared<V>::Cta &to = sh.cta[par][r];
-#pragma unroll
-      for (uint32_t k = 0; k < kMaxCluster; ++k) {
-        if (k >= S) break;
-        const uint32_t there = cluster_map(bar, k);
-        st_async(cluster_map(smem_u32(&to.A[ch]), k), ta, there);
-        st_async(cluster_map(smem_u32(&to.B[ch]), k), tb, there);
+      if (threadIdx.x == 0) mbar_arrive_expect_tx(bar, S * (8 * Sh::C + 4));
+      typename Sh::Cta &to = sh.cta[par][r];
+      const uint32_t here = smem_u32(&to.A[ch]);
+      for (uint32_t k = 0; k < S; ++k) {
+        const uint32_t there = cluster_map(bar, k), dst = cluster_map(here, k);
+        st_async(dst, ta, there);
+        st_async(dst + 4 * Sh::C, tb, there);
         const float flag[1] = {ts ? 1.f : 0.f};
-        if (threadIdx.x == 0) st_async(cluster_map(smem_u32(&to.start), k), flag, there);
+        if (threadIdx.x == 0) st_async(dst + 8 * Sh::C, flag, there);
       }
       // (after a wait that gave up the rounds go on without waiting; the result is undefined)
       mbar_wait(bar, (uint32_t)(round >> 1) & 1u, AbortFlag{&sh.abort, err_word, ERRBIT_SCAN_TIMEOUT});
-    }
-    float v = carry;
-    if (S > 1) {
       float mine = 0.f;
 #pragma unroll
       for (uint32_t k = 0; k < kMaxCluster; ++k) {
         if (k >= S) break;
-        const typename Shared<V>::Cta &m = sh.cta[round & 1][k];
+        const typename Sh::Cta &m = sh.cta[par][k];
         if (k == r) mine = v;
         v = m.start != 0.f ? m.B[ch] : fmaf(m.A[ch], v, m.B[ch]);
       }
@@ -402,14 +401,24 @@ __device__ __forceinline__ void join(Shared<V> &sh, int round, uint32_t S, uint3
       v = mine;
     }
 #pragma unroll
-    for (int w = 0; w < kW; ++w) {
+    for (int w = 0; w < Sh::SEGS; ++w) {
       sh.U[w][ch] = v;
       v = after(w, v);
     }
     if (S == 1) carry = v;
   }
   __syncthreads();
-  to_f32(ld_raw<float, V>(&sh.U[warp][lane * V]), u);
+  to_f32(ld_raw<float, V>(&sh.U[seg][li * V]), u);
+}
+
+// Group g's value of a variable of the whole warp's groups (G = 1: the warp's).
+template <int G>
+__device__ __forceinline__ int of_group(int v, int g) {
+  return G == 1 ? v : __shfl_sync(0xffffffffu, v, g * (32 / G));
+}
+template <int G>
+__device__ __forceinline__ bool all_of(bool b) {
+  return G == 1 ? b : __all_sync(0xffffffffu, b);
 }
 
 // Sequences without a token keep their state: to[n] = from[n] (or 0), spread over the warps
@@ -425,7 +434,7 @@ __device__ __forceinline__ void copy_empty(const int32_t *__restrict__ cu, int n
   }
 }
 
-template <typename TX, typename TG, bool LOGITS, int V, int LS>
+template <typename TX, typename TG, bool LOGITS, int V, int LS, int G>
 __global__ void __launch_bounds__(kW * 32, 2) recurrence_kernel(RecurrenceLaunch p, Parts parts) {
   using RX = Ring<TX, V, LS>;
   using RG = Ring<TG, V, LS>;
@@ -433,21 +442,23 @@ __global__ void __launch_bounds__(kW * 32, 2) recurrence_kernel(RecurrenceLaunch
   extern __shared__ __align__(16) uint8_t smem[];
   RX rx(smem);
   RG rg(smem + STAGES * RX::BYTES);
-  Shared<V> &sh = *reinterpret_cast<Shared<V> *>(smem + STAGES * (RX::BYTES + RG::BYTES));
+  Shared<V, G> &sh = *reinterpret_cast<Shared<V, G> *>(smem + STAGES * (RX::BYTES + RG::BYTES));
   // (from lane 0: the compiler then keeps token indices and row pointers in uniform registers)
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t S = cluster_size(), r = cluster_rank();
-  const int c = (int)(blockIdx.x / S) * 32 * V + lane * V;
+  constexpr int LPG = 32 / G, SEGS = kW * G;
+  const int grp = G == 1 ? 0 : lane / LPG, li = lane % LPG, seg = warp * G + grp;
+  const int c = ((int)(blockIdx.x / S) * LPG + li) * V;
   const bool live = c < p.C;
   const int tb = parts.lo[blockIdx.y], te = parts.hi[blockIdx.y];
-  const int chunk = (int)S * kW * LS;
+  const int chunk = (int)S * SEGS * LS;
   pdl_trigger();
   begin(sh, S);
   pdl_wait();
   // lanes past the last channel load the last ones and store nothing
   const int cl = live ? c : p.C - V;
   const bool put_y = live && p.y;
-  int t0 = tb + (int)r * kW * LS + warp * LS;
+  int t0 = tb + ((int)r * SEGS + seg) * LS;
   const TX *px = reinterpret_cast<const TX *>(p.x) + (int64_t)t0 * p.x_stride + cl;
   const TG *pg = reinterpret_cast<const TG *>(p.gate) + (int64_t)t0 * p.gate_stride + cl;
   TX *py = reinterpret_cast<TX *>(p.y) + (int64_t)t0 * p.y_stride + cl;
@@ -466,7 +477,7 @@ __global__ void __launch_bounds__(kW * 32, 2) recurrence_kernel(RecurrenceLaunch
 #pragma unroll 1
   for (int i = 0; i < STAGES - 1; ++i) fetch(i);
   if (parts.some_empty)
-    copy_empty<V>(p.cu, p.n_seqs, (int)((blockIdx.y * S + r) * kW) + warp, (int)(gridDim.y * S * kW), c,
+    copy_empty<V>(p.cu, p.n_seqs, (int)((blockIdx.y * S + r) * SEGS) + seg, (int)(gridDim.y * S * SEGS), c,
                   live, p.C, p.h0, p.h_final);
 #pragma unroll 1
   for (int tr0 = tb; tr0 < te; tr0 += chunk, t0 += chunk, py += chunk * p.y_stride, ++round) {
@@ -482,7 +493,19 @@ __global__ void __launch_bounds__(kW * 32, 2) recurrence_kernel(RecurrenceLaunch
       decay<LOGITS>(g, a[i]);
     }
     uint32_t mask = 0;
-    if (lim > 0 && (t0 <= from || t0 + LS >= to)) mask = lookup_up(p.cu, p.n_seqs, t0, LS, seq, from, to);
+    const bool look = lim > 0 && (t0 <= from || t0 + LS >= to);
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      if (!of_group<G>(look, g)) continue;
+      int sq = of_group<G>(seq, g), f, t;
+      const uint32_t m = lookup_up(p.cu, p.n_seqs, of_group<G>(t0, g), LS, sq, f, t);
+      if (grp == g) {
+        mask = m;
+        seq = sq;
+        from = f;
+        to = t;
+      }
+    }
     const bool whole = lim == LS && (mask & ~(1u << LS)) == 0;   // of one sequence, begun before
     float A[V], B[V], u[V];
 #pragma unroll
@@ -498,13 +521,13 @@ __global__ void __launch_bounds__(kW * 32, 2) recurrence_kernel(RecurrenceLaunch
 #pragma unroll
       for (int v = 0; v < V; ++v) p.h_final[(int64_t)n * p.C + c + v] = h[v];
     };
-    if (whole) {
+    if (all_of<G>(whole)) {
 #pragma unroll
       for (int i = 0; i < LS; ++i) {
         vfma(B, a[i], B, x[i]);
         vmul(A, A, a[i]);
       }
-      join<V>(sh, round, S, r, p.err_word, A, B, false, carry, u);
+      join<V, G>(sh, round, S, r, p.err_word, seg, li, A, B, false, carry, u);
 #pragma unroll
       for (int i = 0; i < LS; ++i) {
         vfma(u, a[i], u, x[i]);
@@ -534,7 +557,7 @@ __global__ void __launch_bounds__(kW * 32, 2) recurrence_kernel(RecurrenceLaunch
           if (mask >> (i + 1) & 1u) put_final(n, B);
         }
       }
-      join<V>(sh, round, S, r, p.err_word, A, B, inside != 0, carry, u);
+      join<V, G>(sh, round, S, r, p.err_word, seg, li, A, B, inside != 0, carry, u);
 #pragma unroll
       for (int i = 0; i < LS; ++i) {
         if (i >= first) continue;
@@ -578,7 +601,7 @@ __global__ void __launch_bounds__(256) recurrence_step_kernel(RecurrenceLaunch p
 
 // The same scan from the last token to the first: segment position i is token t1 - i, and a
 // sequence "begins" at its last token.
-template <typename TX, typename TG, bool LOGITS, int V, int LS>
+template <typename TX, typename TG, bool LOGITS, int V, int LS, int G>
 __global__ void __launch_bounds__(kW * 32, 2) recurrence_grad_kernel(RecurrenceGradLaunch p, Parts parts) {
   using RX = Ring<TX, V, LS>;
   using RG = Ring<TG, V, LS>;
@@ -586,19 +609,21 @@ __global__ void __launch_bounds__(kW * 32, 2) recurrence_grad_kernel(RecurrenceG
   extern __shared__ __align__(16) uint8_t smem[];
   RX rd(smem), rh(smem + STAGES * RX::BYTES);
   RG rg(smem + 2 * STAGES * RX::BYTES);
-  Shared<V> &sh = *reinterpret_cast<Shared<V> *>(smem + STAGES * (2 * RX::BYTES + RG::BYTES));
+  Shared<V, G> &sh = *reinterpret_cast<Shared<V, G> *>(smem + STAGES * (2 * RX::BYTES + RG::BYTES));
   // (from lane 0: the compiler then keeps token indices and row pointers in uniform registers)
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t S = cluster_size(), r = cluster_rank();
-  const int c = (int)(blockIdx.x / S) * 32 * V + lane * V;
+  constexpr int LPG = 32 / G, SEGS = kW * G;
+  const int grp = G == 1 ? 0 : lane / LPG, li = lane % LPG, seg = warp * G + grp;
+  const int c = ((int)(blockIdx.x / S) * LPG + li) * V;
   const bool live = c < p.C;
   const int tb = parts.lo[blockIdx.y], te = parts.hi[blockIdx.y];
-  const int chunk = (int)S * kW * LS;
+  const int chunk = (int)S * SEGS * LS;
   pdl_trigger();
   begin(sh, S);
   pdl_wait();
   const int cl = live ? c : p.C - V;
-  int t1 = te - 1 - ((int)r * kW * LS + warp * LS);
+  int t1 = te - 1 - ((int)r * SEGS + seg) * LS;
   const TX *pd = reinterpret_cast<const TX *>(p.dy) + (int64_t)t1 * p.dy_stride + cl;
   const TG *pg = reinterpret_cast<const TG *>(p.gate) + (int64_t)t1 * p.gate_stride + cl;
   const TX *ph = reinterpret_cast<const TX *>(p.y) + (int64_t)(t1 - 1) * p.y_stride + cl;   // h_{t-1}
@@ -631,8 +656,19 @@ __global__ void __launch_bounds__(kW * 32, 2) recurrence_grad_kernel(RecurrenceG
     // starts of the tokens [t0, t1 + 1]: token t ends its sequence when t + 1 starts one
     const int t0 = t1 - lim + 1;
     uint32_t mask = 0;
-    if (lim > 0 && (t0 <= from || t1 + 1 >= to))
-      mask = lookup_down(p.cu, low, seq + 1, t0, lim, seq, from, to);
+    const bool look = lim > 0 && (t0 <= from || t1 + 1 >= to);
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      if (!of_group<G>(look, g)) continue;
+      int sq, f, t;
+      const uint32_t m = lookup_down(p.cu, low, of_group<G>(seq, g) + 1, of_group<G>(t0, g), of_group<G>(lim, g), sq, f, t);
+      if (grp == g) {
+        mask = m;
+        seq = sq;
+        from = f;
+        to = t;
+      }
+    }
     // the sequence that holds token t (t0 <= t <= t1): the last one that begins at or before it
     auto seq_of = [&](int t) {
       int n = seq;
@@ -682,14 +718,14 @@ __global__ void __launch_bounds__(kW * 32, 2) recurrence_grad_kernel(RecurrenceG
 #pragma unroll
       for (int v = 0; v < V; ++v) p.dh0[(int64_t)n * p.C + c + v] = uu[v];
     };
-    if (lim == LS && mask == 0) {
+    if (all_of<G>(lim == LS && mask == 0)) {
 #pragma unroll
       for (int i = 0; i < LS; ++i) {
         vadd(B, d[i], B);
         vmul(B, a[i], B);
         vmul(A, A, a[i]);
       }
-      join<V>(sh, round, S, r, p.err_word, A, B, false, carry, u);
+      join<V, G>(sh, round, S, r, p.err_word, seg, li, A, B, false, carry, u);
 #pragma unroll
       for (int i = 0; i < LS; ++i) emit(i, u);
     } else {
@@ -712,7 +748,7 @@ __global__ void __launch_bounds__(kW * 32, 2) recurrence_grad_kernel(RecurrenceG
         emit(i, B);
         put_first(i, B);
       }
-      join<V>(sh, round, S, r, p.err_word, A, B, ends != 0, carry, u);
+      join<V, G>(sh, round, S, r, p.err_word, seg, li, A, B, ends != 0, carry, u);
 #pragma unroll
       for (int i = 0; i < LS; ++i)
         if (i < first) {
@@ -726,10 +762,11 @@ __global__ void __launch_bounds__(kW * 32, 2) recurrence_grad_kernel(RecurrenceG
 }
 
 // How a call is spread: runs of whole sequences (grid.y) times S CTAs of a cluster that share a
-// run's tokens, for `tiles` channel tiles.  Two CTAs run on an SM at a time.  Runs come first
-// (they exchange nothing): up to eight times as many as run at once, the longest first, so that
-// the GPU's own scheduling balances them.  A cluster takes up what is left: a run longer than
-// its fair share of the tokens.
+// run's tokens, for `tiles` channel tiles, with `chunk1` tokens of a CTA in a round.  Two CTAs run
+// on an SM at a time (`want` a tile).  Runs come first (they exchange nothing): up to eight times
+// as many as run at once where each still has eight rounds, the longest first, so that the GPU's
+// own scheduling balances them.  A cluster takes up what is left: a run longer than its fair
+// share of the tokens, or CTAs that would not run at all.
 struct Spread {
   int P, S;
   Parts parts;
@@ -737,8 +774,9 @@ struct Spread {
 };
 Spread spread(const int32_t *cu, int n_seqs, int64_t T, int tiles, int chunk1) {
   Spread sp{};
-  const int64_t want = std::max<int64_t>(1, 2 * device_sm_count() / std::max(1, tiles));
-  const int64_t goal = std::max<int64_t>({T / (8 * want), 2 * (int64_t)chunk1, T / (kMaxParts - 1) + 1});
+  const int64_t slots = 2 * device_sm_count(), want = std::max<int64_t>(1, slots / std::max(1, tiles));
+  const int64_t goal = std::max<int64_t>({T / (8 * want), std::min<int64_t>(T / want + 1, 8 * chunk1),
+                                          T / (kMaxParts - 1) + 1});
   struct Run {
     int32_t lo, hi, seq_lo, seq_hi;
   } runs[kMaxParts];
@@ -761,16 +799,19 @@ Spread spread(const int32_t *cu, int n_seqs, int64_t T, int tiles, int chunk1) {
   }
   sp.P = P;
   const int64_t most = runs[0].hi - runs[0].lo, fair = T / want + 1;
-  sp.S = 1;
-  while (sp.S < kMaxCluster && 4 * most > 5 * sp.S * fair && most > (int64_t)sp.S * chunk1) sp.S *= 2;
+  for (sp.S = 1; sp.S < kMaxCluster; sp.S *= 2) {
+    const int64_t rounds = (most + sp.S * chunk1 - 1) / (sp.S * chunk1);
+    const bool fits = 2 * sp.ctas(tiles) <= slots;
+    if (!(fits && rounds > 4) && !(4 * most > 5 * sp.S * fair && rounds > 8)) break;
+  }
   return sp;
 }
 
 // `stage`: bytes of a round's operands in a CTA
-template <int V, typename Launch>
+template <int V, int G, typename Launch>
 cudaError_t launch_spread(void (*kern)(Launch, Parts), const Launch &p, const Spread &sp, int tiles, int stage,
                           cudaStream_t s, bool pdl) {
-  const size_t smem = (size_t)stages_of(stage) * stage + shared_bytes<V>(sp.S);
+  const size_t smem = (size_t)stages_of(stage) * stage + shared_bytes<V, G>(sp.S);
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[2];
@@ -790,10 +831,22 @@ cudaError_t launch_spread(void (*kern)(Launch, Parts), const Launch &p, const Sp
   return cudaLaunchKernelEx(&cfg, kern, p, sp.parts);
 }
 
+// Launches `kern` (V channels a lane, segments of LS tokens, G groups of lanes a warp; `tok` bytes
+// of operands per token and channel) if that makes CTAs enough to fill three quarters of the GPU
+// (and, with `alone`, needs no cluster), or if it is the last choice.
+template <int V, int LS, int G, typename Launch>
+bool choose(void (*kern)(Launch, Parts), const Launch &p, int tok, bool alone, bool last, cudaStream_t s, bool pdl,
+            cudaError_t *e) {
+  const int tiles = (p.C + 32 / G * V - 1) / (32 / G * V);
+  const Spread sp = spread(p.cu_host, p.n_seqs, p.T, tiles, kW * G * LS);
+  if (!last && (sp.ctas(tiles) * 2 < 3 * device_sm_count() || (alone && sp.S > 1))) return false;
+  *e = launch_spread<V, G>(kern, p, sp, tiles, kW * 32 * V * LS * tok, s, pdl);
+  return true;
+}
+
 bool vec_ok(const void *p, int64_t stride, int elem, int V) {
   return (reinterpret_cast<uintptr_t>(p) % (uintptr_t)(V * elem)) == 0 && stride % V == 0;
 }
-int tiles_of(int C, int V) { return (C + 32 * V - 1) / (32 * V); }
 
 template <typename TX, typename TG, bool LOGITS>
 cudaError_t go(const RecurrenceLaunch &p, cudaStream_t s, bool pdl) {
@@ -811,37 +864,41 @@ cudaError_t go(const RecurrenceLaunch &p, cudaStream_t s, bool pdl) {
                 : launch_kernel(recurrence_step_kernel<TX, TG, LOGITS, 1>, grid, dim3(256), 0, s, pdl, p);
   }
   // segments of 32 elements a thread where both operands have two bytes, else of 16
-  constexpr int kTok = sizeof(TX) + sizeof(TG);
-  constexpr bool kBoth16 = kTok == 4;
-  constexpr int LS2 = kBoth16 ? 16 : 8;
-  if constexpr (kBoth16) {
-    // four channels a lane take fewer instructions, where the wider tiles still fill the GPU (and
-    // need no cluster, whose maps would leave room for one CTA on an SM only)
-    const int tiles = tiles_of(p.C, 4);
-    if (fits(4)) {
-      const Spread sp = spread(p.cu_host, p.n_seqs, p.T, tiles, kW * 8);
-      if (sp.S == 1 && sp.ctas(tiles) * 2 >= 3 * device_sm_count())
-        return launch_spread<4>(recurrence_kernel<TX, TG, LOGITS, 4, 8>, p, sp, tiles, kW * 32 * 4 * 8 * kTok, s, pdl);
-    }
+  constexpr int kTok = sizeof(TX) + sizeof(TG), kElems = kTok == 4 ? 32 : 16;
+  // Four channels a lane take the fewest instructions, in tiles of 128 (16384 x 4096, 40 sequences,
+  // bf16 and fp32 gates: 87 us; two in tiles of 64: 103); narrower tiles where those would be too
+  // few or would need a cluster (16384 x 4096 in one sequence, fp32: 178 us, 147 with two channels
+  // a lane; 65536 x 1024 in one sequence, bf16: 229 us in tiles of 64, 153 in tiles of 32).
+  cudaError_t e = cudaSuccess;
+  if (fits(4) && choose<4, kElems / 4, 1>(recurrence_kernel<TX, TG, LOGITS, 4, kElems / 4, 1>, p, kTok, true, false, s, pdl, &e))
+    return e;
+  if (!fits(2)) {
+    choose<1, 16, 1>(recurrence_kernel<TX, TG, LOGITS, 1, 16, 1>, p, kTok, false, true, s, pdl, &e);
+  } else if (!choose<2, kElems / 2, 1>(recurrence_kernel<TX, TG, LOGITS, 2, kElems / 2, 1>, p, kTok, false, false, s, pdl, &e)) {
+    choose<2, kElems / 2, 2>(recurrence_kernel<TX, TG, LOGITS, 2, kElems / 2, 2>, p, kTok, false, true, s, pdl, &e);
   }
-  const bool two = fits(2);
-  const int tiles = tiles_of(p.C, two ? 2 : 1);
-  const Spread sp = spread(p.cu_host, p.n_seqs, p.T, tiles, kW * (two ? LS2 : 16));
-  return two ? launch_spread<2>(recurrence_kernel<TX, TG, LOGITS, 2, LS2>, p, sp, tiles, kW * 32 * 2 * LS2 * kTok, s, pdl)
-             : launch_spread<1>(recurrence_kernel<TX, TG, LOGITS, 1, 16>, p, sp, tiles, kW * 32 * 16 * kTok, s, pdl);
+  return e;
 }
 
 template <typename TX, typename TG, bool LOGITS>
 cudaError_t go(const RecurrenceGradLaunch &p, cudaStream_t s, bool pdl) {
-  const bool two = p.C % 2 == 0 && vec_ok(p.dy, p.dy_stride, sizeof(TX), 2) &&
-                   vec_ok(p.gate, p.gate_stride, sizeof(TG), 2) && vec_ok(p.y, p.y_stride, sizeof(TX), 2) &&
-                   vec_ok(p.dx, p.dx_stride, sizeof(TX), 2) && vec_ok(p.dgate, p.dgate_stride, sizeof(TG), 2);
-  constexpr int LS = 8;
-  const int tiles = tiles_of(p.C, two ? 2 : 1);
-  const Spread sp = spread(p.cu_host, p.n_seqs, p.T, tiles, kW * LS);
+  auto fits = [&](int V) {
+    return p.C % V == 0 && vec_ok(p.dy, p.dy_stride, sizeof(TX), V) && vec_ok(p.gate, p.gate_stride, sizeof(TG), V) &&
+           vec_ok(p.y, p.y_stride, sizeof(TX), V) && vec_ok(p.dx, p.dx_stride, sizeof(TX), V) &&
+           vec_ok(p.dgate, p.dgate_stride, sizeof(TG), V);
+  };
   constexpr int kTok = 2 * sizeof(TX) + sizeof(TG);
-  return two ? launch_spread<2>(recurrence_grad_kernel<TX, TG, LOGITS, 2, LS>, p, sp, tiles, kW * 32 * 2 * LS * kTok, s, pdl)
-             : launch_spread<1>(recurrence_grad_kernel<TX, TG, LOGITS, 1, LS>, p, sp, tiles, kW * 32 * LS * kTok, s, pdl);
+  // As above, in tiles of 64 (16384 x 4096, 40 sequences, fp32: 209 us; 246 in tiles of 128, 269
+  // with two channels a lane) or 32 (20000 x 256 in three sequences: 59 us, 92 in tiles of 64).
+  cudaError_t e = cudaSuccess;
+  if (fits(4) && choose<4, 4, 2>(recurrence_grad_kernel<TX, TG, LOGITS, 4, 4, 2>, p, kTok, false, false, s, pdl, &e))
+    return e;
+  if (!fits(2)) {
+    choose<1, 8, 1>(recurrence_grad_kernel<TX, TG, LOGITS, 1, 8, 1>, p, kTok, false, true, s, pdl, &e);
+  } else if (!choose<2, 8, 1>(recurrence_grad_kernel<TX, TG, LOGITS, 2, 8, 1>, p, kTok, false, false, s, pdl, &e)) {
+    choose<2, 8, 2>(recurrence_grad_kernel<TX, TG, LOGITS, 2, 8, 2>, p, kTok, false, true, s, pdl, &e);
+  }
+  return e;
 }
 
 template <typename Launch>
