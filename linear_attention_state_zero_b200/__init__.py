@@ -201,7 +201,9 @@ def _seqlens(cu_seqlens, device):
     """(host int32 tensor, device int32 tensor) for a cu_seqlens given either way."""
     if isinstance(cu_seqlens, tuple) and len(cu_seqlens) == 2:
         host, dev = cu_seqlens
-        if host.device.type != "cpu" or dev.device != torch.device(device) or \
+        if not isinstance(device, torch.device):
+            device = torch.device(device)
+        if host.device.type != "cpu" or dev.device != device or \
                 host.dtype != torch.int32 or dev.dtype != torch.int32:
             raise ValueError("a (host, device) cu_seqlens pair must hold int32 tensors")
         return host, dev
@@ -627,14 +629,6 @@ def _matrix(name, t):
     return t.shape
 
 
-def _empty(shape, dtype, like):
-    """An uninitialised packed tensor on like's device (empty_like, where it makes the same
-    tensor, takes 1 us less)."""
-    if like.shape == shape and like.is_contiguous():
-        return torch.empty_like(like, dtype=dtype)
-    return torch.empty(shape, dtype=dtype, device=like.device)
-
-
 def _blocks128(n):
     return (n + 127) // 128
 
@@ -660,12 +654,12 @@ def rmsnorm_fp8(x, gain=None, eps=0.0, *, residual=None, q=None, scale=None, res
         raise ValueError("residual_out without a residual")
 
     def call(handle):
-        qq = q if q is not None else _empty((T, D), _FP8, x)
-        sc = scale if scale is not None else torch.empty((T, _blocks128(D)), dtype=torch.float32,
+        qq = q if q is not None else torch.empty(T, D, dtype=_FP8, device=dev)
+        sc = scale if scale is not None else torch.empty(T, _blocks128(D), dtype=torch.float32,
                                                          device=dev)
         out = residual_out
         if residual is not None and out is None:
-            out = _empty((T, D), residual.dtype, residual)
+            out = torch.empty(T, D, dtype=residual.dtype, device=dev)
         _ok(lib.tr_rmsnorm_fp8(x.data_ptr(), _DTYPES[x.dtype], xs, _ptr(residual), rd, rs,
                                _ptr(gain), T, D, float(eps), qq.data_ptr(), sc.data_ptr(),
                                _ptr(out), ro, handle), "tr_rmsnorm_fp8")
@@ -686,8 +680,8 @@ def quantize_fp8(x, *, block_rows=1, q=None, scale=None, stream=None):
     _need_layout("scale", scale, torch.float32, sshape)
 
     def call(handle):
-        qq = q if q is not None else _empty((R, C), _FP8, x)
-        sc = scale if scale is not None else torch.empty(sshape, dtype=torch.float32, device=dev)
+        qq = q if q is not None else torch.empty(R, C, dtype=_FP8, device=dev)
+        sc = scale if scale is not None else torch.empty(*sshape, dtype=torch.float32, device=dev)
         _ok(lib.tr_quantize_fp8(x.data_ptr(), _DTYPES[x.dtype], xs, R, C, block_rows, qq.data_ptr(),
                                 sc.data_ptr(), handle), "tr_quantize_fp8")
         return qq, sc
@@ -712,7 +706,7 @@ def projection_fp8(a, a_scale, w, w_scale, *, out_dtype=torch.bfloat16, y=None, 
         raise TypeError("unsupported dtype %s" % out_dtype)
 
     def call(handle):
-        out = y if y is not None else torch.empty((T, N), dtype=out_dtype, device=dev)
+        out = y if y is not None else torch.empty(T, N, dtype=out_dtype, device=dev)
         _ok(lib.tr_projection_fp8(a.data_ptr(), as_, a_scale.data_ptr(), w.data_ptr(), ws,
                                   w_scale.data_ptr(), T, N, K, out.data_ptr(), _DTYPES[out_dtype],
                                   ys, handle), "tr_projection_fp8")
@@ -745,10 +739,9 @@ def linear_recurrence(x, gate, cu_seqlens, *, h0=None, gate_logits=False, want_y
         N = host.numel() - 1
         _need_layout("h0", h0, torch.float32, (N, C))
         _need_layout("h_final", h_final, torch.float32, (N, C))
-        out = (y if y is not None else _empty((T, C), x.dtype, x)) if want_y else None
-        fin = h_final
-        if fin is None:
-            fin = _empty((N, C), torch.float32, x if h0 is None else h0)
+        out = (y if y is not None else torch.empty(T, C, dtype=x.dtype, device=dev)) \
+            if want_y else None
+        fin = h_final if h_final is not None else torch.empty(N, C, dtype=torch.float32, device=dev)
         a = RecurrenceArgs(N, C, T, _DTYPES[x.dtype], _DTYPES[gate.dtype],
                            TR_GATE_LOGITS if gate_logits else 0, xs, gs, ys, x.data_ptr(),
                            gate.data_ptr(), cu.data_ptr(), host.data_ptr(), _ptr(h0), _ptr(out),
@@ -779,13 +772,11 @@ def linear_recurrence_backward(dy, gate, y, cu_seqlens, *, h0=None, dh_final=Non
         N = host.numel() - 1
         for name, t in (("h0", h0), ("dh_final", dh_final), ("dh0", dh0)):
             _need_layout(name, t, torch.float32, (N, C))
-        ox = dx if dx is not None else _empty((T, C), dy.dtype, dy)
-        og = dgate if dgate is not None else _empty((T, C), gate.dtype, gate)
+        ox = dx if dx is not None else torch.empty(T, C, dtype=dy.dtype, device=dev)
+        og = dgate if dgate is not None else torch.empty(T, C, dtype=gate.dtype, device=dev)
         oh = None
         if want_dh0:
-            oh = dh0
-            if oh is None:
-                oh = _empty((N, C), torch.float32, dy if h0 is None else h0)
+            oh = dh0 if dh0 is not None else torch.empty(N, C, dtype=torch.float32, device=dev)
         a = RecurrenceGradArgs(N, C, T, _DTYPES[dy.dtype], _DTYPES[gate.dtype],
                                TR_GATE_LOGITS if gate_logits else 0, ds, gs, ys, dxs, dgs,
                                dy.data_ptr(), gate.data_ptr(), y.data_ptr(), cu.data_ptr(),
