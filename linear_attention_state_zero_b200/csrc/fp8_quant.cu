@@ -27,22 +27,39 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
-template <bool BF16>
-__device__ __forceinline__ void load8(const void *p, int64_t off, float (&f)[8]) {
-  if (BF16) {
-    const uint4 u = *reinterpret_cast<const uint4 *>(reinterpret_cast<const __nv_bfloat16 *>(p) + off);
+// 8 elements as loaded
+template <bool BF16> struct Raw8;
+template <> struct Raw8<true> {
+  uint4 u;
+  __device__ __forceinline__ void load(const void *p, int64_t off) {
+    u = *reinterpret_cast<const uint4 *>(reinterpret_cast<const __nv_bfloat16 *>(p) + off);
+  }
+  __device__ __forceinline__ void to_f32(float (&f)[8]) const {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       f[2 * i] = __uint_as_float(w[i] << 16);
       f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
-  } else {
+  }
+};
+template <> struct Raw8<false> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const void *p, int64_t off) {
     const float4 *q = reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(p) + off);
-    const float4 a = q[0], b = q[1];
+    a = q[0];
+    b = q[1];
+  }
+  __device__ __forceinline__ void to_f32(float (&f)[8]) const {
     f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
     f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
   }
+};
+template <bool BF16>
+__device__ __forceinline__ void load8(const void *p, int64_t off, float (&f)[8]) {
+  Raw8<BF16> r;
+  r.load(p, off);
+  r.to_f32(f);
 }
 
 template <bool BF16>
@@ -89,6 +106,7 @@ constexpr int kNV = 4;   // 8-element vectors a lane holds of its row
 // warp (v / 32) % WPR, so 16 neighbouring lanes hold a scale block and each warp's accesses
 // are contiguous.  A few vectors per lane and several warps per row, rather than a warp per
 // row with the whole row in its registers, so that a few rows use many warps too.
+// A vector's division is done by one lane in four, as in quantize_rows_kernel.
 template <bool XBF, bool RES, bool RBF, int WPR>
 __global__ void __launch_bounds__(WPR < 8 ? 256 : WPR * 32)
     rmsnorm_fp8_kernel(NormFp8Launch p) {
@@ -102,9 +120,10 @@ __global__ void __launch_bounds__(WPR < 8 ? 256 : WPR * 32)
   pdl_wait();
   float f[kNV][8];
   float ss = 0.f;
+  auto first = [&](int j) { return (j * WPR + wr) * 256; };   // a vector's first column in the warp
 #pragma unroll
   for (int j = 0; j < kNV; ++j) {
-    const int c = ((j * WPR + wr) * 32 + lane) * 8;
+    const int c = first(j) + lane * 8;
     const bool in = live && c < p.D;
     if (in) load8<XBF>(p.x, row * p.x_stride + c, f[j]);
     else {
@@ -120,7 +139,7 @@ __global__ void __launch_bounds__(WPR < 8 ? 256 : WPR * 32)
   }
 #pragma unroll
   for (int j = 0; j < kNV; ++j) {
-    const int c = ((j * WPR + wr) * 32 + lane) * 8;
+    const int c = first(j) + lane * 8;
     if (RES && p.res_out && live && c < p.D)
       store8<RBF>(p.res_out, row * p.res_out_stride + c, f[j]);
 #pragma unroll
@@ -137,9 +156,10 @@ __global__ void __launch_bounds__(WPR < 8 ? 256 : WPR * 32)
   }
   const float rms = rsqrtf(ss / (float)p.D + p.eps);
   const int kb = (p.D + kScaleBlock - 1) / kScaleBlock;
+  float mine = 0.f;
 #pragma unroll
   for (int j = 0; j < kNV; ++j) {
-    const int c = ((j * WPR + wr) * 32 + lane) * 8;
+    const int c = first(j) + lane * 8;
     const bool in = live && c < p.D;
     float g[8];
     if (p.gain && in) load8<false>(p.gain, c, g);
@@ -152,9 +172,16 @@ __global__ void __launch_bounds__(WPR < 8 ? 256 : WPR * 32)
     float m = abs_max8(f[j]);
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const float s = scale_of(m);
-    if (in) {
-      store_q8(p.q + row * p.D + c, f[j], __frcp_rn(s));
+    if (lane % kNV == j) mine = m;
+  }
+  const float my_scale = scale_of(mine), my_inv = __frcp_rn(my_scale);
+#pragma unroll
+  for (int j = 0; j < kNV; ++j) {
+    const int c = first(j) + lane * 8;
+    const float s = __shfl_sync(0xffffffffu, my_scale, (lane & 16) + j);
+    const float inv = __shfl_sync(0xffffffffu, my_inv, (lane & 16) + j);
+    if (live && c < p.D) {
+      store_q8(p.q + row * p.D + c, f[j], inv);
       if ((lane & 15) == 0) p.scale[row * kb + c / kScaleBlock] = s;
     }
   }
@@ -206,8 +233,8 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(QuantFp8Launch p) {
   }
 }
 
-// One scale per 128 x 128 tile: a block holds the tile in registers, 8 rows per thread
-// (16 lanes across the columns, 16 row groups).
+// One scale per 128 x 128 tile: a block holds the tile in registers as it was loaded, 8 rows per
+// thread (16 lanes across the columns, 16 row groups).
 template <bool XBF>
 __global__ void __launch_bounds__(256) quantize_tile_kernel(QuantFp8Launch p) {
   __shared__ float part[8];
@@ -218,18 +245,19 @@ __global__ void __launch_bounds__(256) quantize_tile_kernel(QuantFp8Launch p) {
   const int64_t r0 = rb * kScaleBlock + (threadIdx.x >> 4);
   pdl_trigger();
   pdl_wait();
-  float f[8][8];
+  Raw8<XBF> raw[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    if (r0 + 16 * j < p.rows && c < p.cols) load8<XBF>(p.x, (r0 + 16 * j) * p.x_stride + c, f[j]);
-    else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) f[j][i] = 0.f;
-    }
+    raw[j] = Raw8<XBF>{};
+    if (r0 + 16 * j < p.rows && c < p.cols) raw[j].load(p.x, (r0 + 16 * j) * p.x_stride + c);
   }
   float m = 0.f;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) m = max_nan(m, abs_max8(f[j]));
+  for (int j = 0; j < 8; ++j) {
+    float f[8];
+    raw[j].to_f32(f);
+    m = max_nan(m, abs_max8(f));
+  }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
   if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
@@ -239,8 +267,11 @@ __global__ void __launch_bounds__(256) quantize_tile_kernel(QuantFp8Launch p) {
   const float s = scale_of(m);
   const float inv = __frcp_rn(s);
 #pragma unroll
-  for (int j = 0; j < 8; ++j)
-    if (r0 + 16 * j < p.rows && c < p.cols) store_q8(p.q + (r0 + 16 * j) * p.cols + c, f[j], inv);
+  for (int j = 0; j < 8; ++j) {
+    float f[8];
+    raw[j].to_f32(f);
+    if (r0 + 16 * j < p.rows && c < p.cols) store_q8(p.q + (r0 + 16 * j) * p.cols + c, f, inv);
+  }
   if (threadIdx.x == 0) p.scale[rb * kb + cb] = s;
 }
 
