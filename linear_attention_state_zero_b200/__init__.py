@@ -167,15 +167,16 @@ def _need_cuda(*ts):
 
     The library launches on the current device, so each call below runs with this device
     made current (``torch.cuda.device``) and on its current stream unless one is given."""
-    dev = None
+    dev, index = None, -1
     for t in ts:
         if t is None:
             continue
         if not t.is_cuda:
             raise ValueError("tensors must live on a CUDA device")
+        i = t.get_device()
         if dev is None:
-            dev = t.device
-        elif t.device != dev:
+            dev, index = t.device, i
+        elif i != index:
             raise ValueError("tensors must live on one device (%s and %s)" % (dev, t.device))
     return dev
 
@@ -590,19 +591,33 @@ _FP8 = torch.float8_e4m3fn
 _DTYPES = {torch.float32: TR_DTYPE_F32, torch.bfloat16: TR_DTYPE_BF16}
 
 
-def _enqueue(dev, stream, call):
-    """call(raw stream handle) with the tensors' device current, on its current stream or on
-    `stream`; what `call` allocates then belongs to the stream that its kernels run on."""
+# What a call of a small operator costs is the host's: 4 us to make a Stream object, 1.7 us for
+# each output that torch.empty allocates, 0.8 us by the allocator's direct entry (where this
+# build of torch has it), 2.5 us for the launch.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_device_index = torch._C._cuda_getDevice
+try:
+    from torch._C._dynamo.guards import _empty_strided_cuda
+except ImportError:
+    def _empty_strided_cuda(shape, strides, dtype):
+        return torch.empty_strided(shape, strides, dtype=dtype, device="cuda")
+
+
+def _matrix_of(rows, cols, dtype):
+    """An uninitialised packed matrix on the current device."""
+    return _empty_strided_cuda((rows, cols), (cols, 1), dtype)
+
+
+def _on(stream, dev, fn, *args, **kw):
+    """fn(*args, **kw) with the tensors' device current, on its current stream or on `stream`;
+    what fn allocates then belongs to the stream that its kernels run on."""
     if stream is None:
-        # the raw handle, without the Stream object around it that takes 4 us to make
-        if torch.cuda.current_device() == dev.index:
-            return call(torch._C._cuda_getCurrentRawStream(dev.index))
         with torch.cuda.device(dev):
-            return call(torch._C._cuda_getCurrentRawStream(dev.index))
+            return fn(*args, **kw)
     if getattr(stream, "device", dev) != dev:
         raise ValueError("the stream belongs to %s, the tensors to %s" % (stream.device, dev))
     with torch.cuda.stream(stream):
-        return call(stream.cuda_stream)
+        return fn(*args, **kw)
 
 
 def _row_stride(name, t, shape, dtypes):
@@ -640,31 +655,33 @@ def rmsnorm_fp8(x, gain=None, eps=0.0, *, residual=None, q=None, scale=None, res
     residual_out may be the residual itself."""
     T, D = _matrix("x", x)
     dev = _need_cuda(x, gain, residual, q, scale, residual_out)
+    if stream is not None or _device_index() != dev.index:
+        return _on(stream, dev, rmsnorm_fp8, x, gain, eps, residual=residual, q=q, scale=scale,
+                   residual_out=residual_out)
     xs = _row_stride("x", x, (T, D), _DTYPES)
     _need_layout("gain", gain, torch.float32, (D,))
-    _need_layout("q", q, _FP8, (T, D))
-    _need_layout("scale", scale, torch.float32, (T, _blocks128(D)))
     rs = ro = rd = 0
     if residual is not None:
         rs = _row_stride("residual", residual, (T, D), _DTYPES)
         rd = _DTYPES[residual.dtype]
-        if residual_out is not None:
+        if residual_out is None:
+            residual_out = _matrix_of(T, D, residual.dtype)
+        else:
             ro = _row_stride("residual_out", residual_out, (T, D), (residual.dtype,))
     elif residual_out is not None:
         raise ValueError("residual_out without a residual")
-
-    def call(handle):
-        qq = q if q is not None else torch.empty(T, D, dtype=_FP8, device=dev)
-        sc = scale if scale is not None else torch.empty(T, _blocks128(D), dtype=torch.float32,
-                                                         device=dev)
-        out = residual_out
-        if residual is not None and out is None:
-            out = torch.empty(T, D, dtype=residual.dtype, device=dev)
-        _ok(lib.tr_rmsnorm_fp8(x.data_ptr(), _DTYPES[x.dtype], xs, _ptr(residual), rd, rs,
-                               _ptr(gain), T, D, float(eps), qq.data_ptr(), sc.data_ptr(),
-                               _ptr(out), ro, handle), "tr_rmsnorm_fp8")
-        return qq, sc, out
-    return _enqueue(dev, stream, call)
+    if q is None:
+        q = _matrix_of(T, D, _FP8)
+    else:
+        _need_layout("q", q, _FP8, (T, D))
+    if scale is None:
+        scale = _matrix_of(T, _blocks128(D), torch.float32)
+    else:
+        _need_layout("scale", scale, torch.float32, (T, _blocks128(D)))
+    _ok(lib.tr_rmsnorm_fp8(x.data_ptr(), _DTYPES[x.dtype], xs, _ptr(residual), rd, rs, _ptr(gain),
+                           T, D, float(eps), q.data_ptr(), scale.data_ptr(), _ptr(residual_out),
+                           ro, _raw_stream(dev.index)), "tr_rmsnorm_fp8")
+    return q, scale, residual_out
 
 
 def quantize_fp8(x, *, block_rows=1, q=None, scale=None, stream=None):
@@ -672,20 +689,23 @@ def quantize_fp8(x, *, block_rows=1, q=None, scale=None, stream=None):
     fp32); block_rows 1 for an activation, 128 for a weight."""
     R, C = _matrix("x", x)
     dev = _need_cuda(x, q, scale)
+    if stream is not None or _device_index() != dev.index:
+        return _on(stream, dev, quantize_fp8, x, block_rows=block_rows, q=q, scale=scale)
     xs = _row_stride("x", x, (R, C), _DTYPES)
     if block_rows not in (1, 128):
         raise ValueError("block_rows must be 1 or 128")
-    sshape = ((R + block_rows - 1) // block_rows, _blocks128(C))
-    _need_layout("q", q, _FP8, (R, C))
-    _need_layout("scale", scale, torch.float32, sshape)
-
-    def call(handle):
-        qq = q if q is not None else torch.empty(R, C, dtype=_FP8, device=dev)
-        sc = scale if scale is not None else torch.empty(*sshape, dtype=torch.float32, device=dev)
-        _ok(lib.tr_quantize_fp8(x.data_ptr(), _DTYPES[x.dtype], xs, R, C, block_rows, qq.data_ptr(),
-                                sc.data_ptr(), handle), "tr_quantize_fp8")
-        return qq, sc
-    return _enqueue(dev, stream, call)
+    rb, cb = (R + block_rows - 1) // block_rows, _blocks128(C)
+    if q is None:
+        q = _matrix_of(R, C, _FP8)
+    else:
+        _need_layout("q", q, _FP8, (R, C))
+    if scale is None:
+        scale = _matrix_of(rb, cb, torch.float32)
+    else:
+        _need_layout("scale", scale, torch.float32, (rb, cb))
+    _ok(lib.tr_quantize_fp8(x.data_ptr(), _DTYPES[x.dtype], xs, R, C, block_rows, q.data_ptr(),
+                            scale.data_ptr(), _raw_stream(dev.index)), "tr_quantize_fp8")
+    return q, scale
 
 
 def projection_fp8(a, a_scale, w, w_scale, *, out_dtype=torch.bfloat16, y=None, stream=None):
@@ -694,6 +714,8 @@ def projection_fp8(a, a_scale, w, w_scale, *, out_dtype=torch.bfloat16, y=None, 
     T, K = _matrix("a", a)
     N = _matrix("w", w)[0]
     dev = _need_cuda(a, a_scale, w, w_scale, y)
+    if stream is not None or _device_index() != dev.index:
+        return _on(stream, dev, projection_fp8, a, a_scale, w, w_scale, out_dtype=out_dtype, y=y)
     as_ = _row_stride("a", a, (T, K), (_FP8,))
     ws = _row_stride("w", w, (N, K), (_FP8,))
     _need_layout("a_scale", a_scale, torch.float32, (T, _blocks128(K)))
@@ -704,14 +726,12 @@ def projection_fp8(a, a_scale, w, w_scale, *, out_dtype=torch.bfloat16, y=None, 
         ys = _row_stride("y", y, (T, N), _DTYPES)
     elif out_dtype not in _DTYPES:
         raise TypeError("unsupported dtype %s" % out_dtype)
-
-    def call(handle):
-        out = y if y is not None else torch.empty(T, N, dtype=out_dtype, device=dev)
-        _ok(lib.tr_projection_fp8(a.data_ptr(), as_, a_scale.data_ptr(), w.data_ptr(), ws,
-                                  w_scale.data_ptr(), T, N, K, out.data_ptr(), _DTYPES[out_dtype],
-                                  ys, handle), "tr_projection_fp8")
-        return out
-    return _enqueue(dev, stream, call)
+    else:
+        y = _matrix_of(T, N, out_dtype)
+    _ok(lib.tr_projection_fp8(a.data_ptr(), as_, a_scale.data_ptr(), w.data_ptr(), ws,
+                              w_scale.data_ptr(), T, N, K, y.data_ptr(), _DTYPES[out_dtype], ys,
+                              _raw_stream(dev.index)), "tr_projection_fp8")
+    return y
 
 
 def _offsets(cu_seqlens, device):
@@ -730,25 +750,29 @@ def linear_recurrence(x, gate, cu_seqlens, *, h0=None, gate_logits=False, want_y
     (None: zero start); h_final may be h0.  For a captured call give cu_seqlens as seqlens()."""
     T, C = _matrix("x", x)
     dev = _need_cuda(x, gate, h0, y, h_final)
+    if stream is not None or _device_index() != dev.index:
+        return _on(stream, dev, linear_recurrence, x, gate, cu_seqlens, h0=h0,
+                   gate_logits=gate_logits, want_y=want_y, y=y, h_final=h_final)
     xs = _row_stride("x", x, (T, C), _DTYPES)
     gs = _row_stride("gate", gate, (T, C), _DTYPES)
     ys = _row_stride("y", y, (T, C), (x.dtype,)) if y is not None else 0
-
-    def call(handle):
-        host, cu = _offsets(cu_seqlens, dev)
-        N = host.numel() - 1
-        _need_layout("h0", h0, torch.float32, (N, C))
+    host, cu = _offsets(cu_seqlens, dev)
+    N = host.shape[0] - 1
+    _need_layout("h0", h0, torch.float32, (N, C))
+    if not want_y:
+        y = None
+    elif y is None:
+        y = _matrix_of(T, C, x.dtype)
+    if h_final is None:
+        h_final = _matrix_of(N, C, torch.float32)
+    else:
         _need_layout("h_final", h_final, torch.float32, (N, C))
-        out = (y if y is not None else torch.empty(T, C, dtype=x.dtype, device=dev)) \
-            if want_y else None
-        fin = h_final if h_final is not None else torch.empty(N, C, dtype=torch.float32, device=dev)
-        a = RecurrenceArgs(N, C, T, _DTYPES[x.dtype], _DTYPES[gate.dtype],
-                           TR_GATE_LOGITS if gate_logits else 0, xs, gs, ys, x.data_ptr(),
-                           gate.data_ptr(), cu.data_ptr(), host.data_ptr(), _ptr(h0), _ptr(out),
-                           fin.data_ptr())
-        _ok(lib.tr_linear_recurrence(ctypes.byref(a), handle), "tr_linear_recurrence")
-        return out, fin
-    return _enqueue(dev, stream, call)
+    a = RecurrenceArgs(N, C, T, _DTYPES[x.dtype], _DTYPES[gate.dtype],
+                       TR_GATE_LOGITS if gate_logits else 0, xs, gs, ys, x.data_ptr(),
+                       gate.data_ptr(), cu.data_ptr(), host.data_ptr(), _ptr(h0), _ptr(y),
+                       h_final.data_ptr())
+    _ok(lib.tr_linear_recurrence(ctypes.byref(a), _raw_stream(dev.index)), "tr_linear_recurrence")
+    return y, h_final
 
 
 def linear_recurrence_backward(dy, gate, y, cu_seqlens, *, h0=None, dh_final=None,
@@ -759,6 +783,10 @@ def linear_recurrence_backward(dy, gate, y, cu_seqlens, *, h0=None, dh_final=Non
     where want_dh0 (by default: where there is an h0 or a dh0 to fill) and may be dh_final."""
     T, C = _matrix("dy", dy)
     dev = _need_cuda(dy, gate, y, h0, dh_final, dx, dgate, dh0)
+    if stream is not None or _device_index() != dev.index:
+        return _on(stream, dev, linear_recurrence_backward, dy, gate, y, cu_seqlens, h0=h0,
+                   dh_final=dh_final, gate_logits=gate_logits, want_dh0=want_dh0, dx=dx,
+                   dgate=dgate, dh0=dh0)
     ds = _row_stride("dy", dy, (T, C), _DTYPES)
     gs = _row_stride("gate", gate, (T, C), _DTYPES)
     ys = _row_stride("y", y, (T, C), (dy.dtype,))
@@ -766,26 +794,26 @@ def linear_recurrence_backward(dy, gate, y, cu_seqlens, *, h0=None, dh_final=Non
     dgs = _row_stride("dgate", dgate, (T, C), (gate.dtype,)) if dgate is not None else 0
     if want_dh0 is None:
         want_dh0 = h0 is not None or dh0 is not None
-
-    def call(handle):
-        host, cu = _offsets(cu_seqlens, dev)
-        N = host.numel() - 1
-        for name, t in (("h0", h0), ("dh_final", dh_final), ("dh0", dh0)):
-            _need_layout(name, t, torch.float32, (N, C))
-        ox = dx if dx is not None else torch.empty(T, C, dtype=dy.dtype, device=dev)
-        og = dgate if dgate is not None else torch.empty(T, C, dtype=gate.dtype, device=dev)
-        oh = None
-        if want_dh0:
-            oh = dh0 if dh0 is not None else torch.empty(N, C, dtype=torch.float32, device=dev)
-        a = RecurrenceGradArgs(N, C, T, _DTYPES[dy.dtype], _DTYPES[gate.dtype],
-                               TR_GATE_LOGITS if gate_logits else 0, ds, gs, ys, dxs, dgs,
-                               dy.data_ptr(), gate.data_ptr(), y.data_ptr(), cu.data_ptr(),
-                               host.data_ptr(), _ptr(h0), _ptr(dh_final), ox.data_ptr(),
-                               og.data_ptr(), _ptr(oh))
-        _ok(lib.tr_linear_recurrence_backward(ctypes.byref(a), handle),
-            "tr_linear_recurrence_backward")
-        return ox, og, oh
-    return _enqueue(dev, stream, call)
+    host, cu = _offsets(cu_seqlens, dev)
+    N = host.shape[0] - 1
+    for name, t in (("h0", h0), ("dh_final", dh_final), ("dh0", dh0)):
+        _need_layout(name, t, torch.float32, (N, C))
+    if dx is None:
+        dx = _matrix_of(T, C, dy.dtype)
+    if dgate is None:
+        dgate = _matrix_of(T, C, gate.dtype)
+    if not want_dh0:
+        dh0 = None
+    elif dh0 is None:
+        dh0 = _matrix_of(N, C, torch.float32)
+    a = RecurrenceGradArgs(N, C, T, _DTYPES[dy.dtype], _DTYPES[gate.dtype],
+                           TR_GATE_LOGITS if gate_logits else 0, ds, gs, ys, dxs, dgs,
+                           dy.data_ptr(), gate.data_ptr(), y.data_ptr(), cu.data_ptr(),
+                           host.data_ptr(), _ptr(h0), _ptr(dh_final), dx.data_ptr(),
+                           dgate.data_ptr(), _ptr(dh0))
+    _ok(lib.tr_linear_recurrence_backward(ctypes.byref(a), _raw_stream(dev.index)),
+        "tr_linear_recurrence_backward")
+    return dx, dgate, dh0
 
 
 def set_wait_limit_ns(ns: int) -> None:
