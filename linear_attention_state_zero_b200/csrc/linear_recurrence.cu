@@ -249,7 +249,9 @@ __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_grou
 template <int N> __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-// Rounds in the rings (the one in hand among them), for stages of `bytes`: two CTAs on an SM.
+// Rounds in the rings (the one in hand among them), for stages of `bytes`.  Two CTAs run on an
+// SM, and copies of less than 16 bytes need the L1 cache while they are in flight: with rings
+// of 96 KB instead of 64 the forward pass over 65536 x 4096 took 360 us instead of 262.
 constexpr int stages_of(int bytes) { return 65536 / bytes > 4 ? 4 : 65536 / bytes < 2 ? 2 : 65536 / bytes; }
 
 // The maps u -> A u + B of a round's segments, per channel, and the values in front of them.
@@ -259,7 +261,7 @@ constexpr int stages_of(int bytes) { return 65536 / bytes > 4 ? 4 : 65536 / byte
 template <int V, int G>
 struct Shared {
   static constexpr int C = 32 / G * V, SEGS = kW * G;
-  float A[SEGS][C], B[SEGS][C], U[SEGS][C];
+  float A[SEGS][C], B[SEGS][C];    // (the value in front of a segment then takes its A's place)
   float start[SEGS];
   uint64_t bar[2];                 // every CTA's maps of a set are here
   int abort;
@@ -402,13 +404,14 @@ __device__ __forceinline__ void join(Shared<V, G> &sh, int round, uint32_t S, ui
     }
 #pragma unroll
     for (int w = 0; w < Sh::SEGS; ++w) {
-      sh.U[w][ch] = v;
+      const float u_w = v;
       v = after(w, v);
+      sh.A[w][ch] = u_w;
     }
     if (S == 1) carry = v;
   }
   __syncthreads();
-  to_f32(ld_raw<float, V>(&sh.U[seg][li * V]), u);
+  to_f32(ld_raw<float, V>(&sh.A[seg][li * V]), u);
 }
 
 // Group g's value of a variable of the whole warp's groups (G = 1: the warp's).
@@ -889,7 +892,9 @@ cudaError_t go(const RecurrenceGradLaunch &p, cudaStream_t s, bool pdl) {
            vec_ok(p.y, p.y_stride, sizeof(TX), V) && vec_ok(p.dx, p.dx_stride, sizeof(TX), V) &&
            vec_ok(p.dgate, p.dgate_stride, sizeof(TG), V);
   };
-  constexpr int kTok = 2 * sizeof(TX) + sizeof(TG);
+  // (at 10 or 12 bytes a token shorter segments: rings of 64 KB; 13130 x 2022, fp32: 105 us, 219
+  // with segments of 8)
+  constexpr int kTok = 2 * sizeof(TX) + sizeof(TG), LS2 = kTok >= 10 ? 4 : 8;
   // As above, in tiles of 64 (16384 x 4096, 40 sequences, fp32: 209 us; 246 in tiles of 128, 269
   // with two channels a lane) or 32 (20000 x 256 in three sequences: 59 us, 92 in tiles of 64).
   cudaError_t e = cudaSuccess;
@@ -897,8 +902,8 @@ cudaError_t go(const RecurrenceGradLaunch &p, cudaStream_t s, bool pdl) {
     return e;
   if (!fits(2)) {
     choose<1, 8, 1>(recurrence_grad_kernel<TX, TG, LOGITS, 1, 8, 1>, p, kTok, false, true, s, pdl, &e);
-  } else if (!choose<2, 8, 1>(recurrence_grad_kernel<TX, TG, LOGITS, 2, 8, 1>, p, kTok, false, false, s, pdl, &e)) {
-    choose<2, 8, 2>(recurrence_grad_kernel<TX, TG, LOGITS, 2, 8, 2>, p, kTok, false, true, s, pdl, &e);
+  } else if (!choose<2, LS2, 1>(recurrence_grad_kernel<TX, TG, LOGITS, 2, LS2, 1>, p, kTok, false, false, s, pdl, &e)) {
+    choose<2, LS2, 2>(recurrence_grad_kernel<TX, TG, LOGITS, 2, LS2, 2>, p, kTok, false, true, s, pdl, &e);
   }
   return e;
 }
