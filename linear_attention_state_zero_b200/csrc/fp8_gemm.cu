@@ -13,9 +13,9 @@
 // gemm_fp8_pair_kernel, for many outputs: a pair of CTAs shares a 256 x BN tile
 // (tcgen05.mma.cta_group::2), so that a block of 128 columns costs each SM (128 + BN / 2) x 128
 // bytes of operands for 128 x BN outputs.  What bounds it is the epilogue: every block is read
-// back from TMEM and added with one FFMA per output, 256 cycles of the FMA pipe at BN = 256, and
-// as many again of waits that its two warps per scheduler do not hide, against 512 cycles of the
-// tensor core's (a block takes 740 cycles in all).  At 13112 x 12352 x 4096 a call takes
+// back from TMEM and added in fp32 registers, 256 cycles of the FMA pipe at BN = 256, and with two
+// buffers of TMEM the way from a buffer's last read over both CTAs' barriers to its next sums is
+// not hidden: a block takes 740 cycles against 512 of the tensor core's (510 at BN = 128).  At 13112 x 12352 x 4096 a call takes
 // 0.71-0.88 ms (1.9-1.5 PFLOP/s, by how far the power limit lowers the clock); a library product
 // with one scale for everything takes 0.47-0.55 ms there.  The first version, tiles of 128 x 128
 // of single CTAs whose products one lane issued, took 1.14 ms.
@@ -331,9 +331,9 @@ __global__ void __launch_bounds__(PairCfg<BN>::THREADS, 1)
       const int row0 = at.m * 2 * BM + (int)rank * BM + q4 * 32;
       const int row = row0 + lane;
       const int c0 = at.n * BN + group * NC;
-      float acc[NC];
+      uint64_t sum[NC / 2];   // two columns each
 #pragma unroll
-      for (int i = 0; i < NC; ++i) acc[i] = 0.f;
+      for (int i = 0; i < NC / 2; ++i) sum[i] = 0;
       // Block kb uses TMEM buffer kb % BUFS, so that the buffer is a constant of the unrolled
       // loop; `phases` holds one bit per buffer.
       auto step = [&](int b, const float *sa, const float *sw) {
@@ -352,7 +352,8 @@ __global__ void __launch_bounds__(PairCfg<BN>::THREADS, 1)
             if (lane == 0) mbar_arrive_cluster_relaxed(tempty0 + (uint32_t)(b * sizeof(uint64_t)));
           }
 #pragma unroll
-          for (int i = 0; i < 16; ++i) acc[16 * j + i] = fmaf(v[i], s, acc[16 * j + i]);
+          for (int i = 0; i < 16; i += 2)
+            sum[8 * j + i / 2] = fma_f32x2(pair_f32(v[i], v[i + 1]), pair_f32(s, s), sum[8 * j + i / 2]);
         }
       };
       // (a wait that gives up does not leave these loops: with an exit in them the sums would be
@@ -375,6 +376,9 @@ __global__ void __launch_bounds__(PairCfg<BN>::THREADS, 1)
         sph ^= sb == 0 ? 1u : 0u;
       }
       if (!ok) break;
+      float acc[NC];
+#pragma unroll
+      for (int i = 0; i < NC; i += 2) split_f32(sum[i / 2], acc[i], acc[i + 1]);
       if (!tma_out) {
         store_row(p, row, c0, acc);
       } else if (row0 < p.T && c0 < p.N) {
@@ -743,7 +747,7 @@ cudaError_t launch_gemm_fp8(const GemmFp8Launch &p, unsigned *err_word, cudaStre
   const int64_t m = (p.T + 2 * BM - 1) / (2 * BM);
   const int64_t w128 = (m * ((p.N + 127) / 128) + pairs - 1) / pairs;
   const int64_t w256 = (m * ((p.N + 255) / 256) + pairs - 1) / pairs;
-  // A block of 128 columns of K takes 740 cycles at BN = 256 and 600 at BN = 128 (4096 x 4736):
+  // A block of 128 columns of K takes 740 cycles at BN = 256 and 510 at BN = 128 (4096 x 4736):
   // the narrow tile only where it needs no more rounds.
   if (w128 <= w256) return launch_pair<128>(p, err_word, s, pdl, err);
   return launch_pair<256>(p, err_word, s, pdl, err);

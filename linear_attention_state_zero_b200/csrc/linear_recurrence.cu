@@ -89,14 +89,6 @@ __device__ __forceinline__ void st_f32(float *p, const float (&f)[V]) {
 }
 
 // d = a b + c, a b and a + b of V channels, two to an instruction (each rounds as the scalar one).
-__device__ __forceinline__ uint64_t pair(float lo, float hi) {
-  uint64_t d;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
-  return d;
-}
-__device__ __forceinline__ void split(uint64_t d, float &lo, float &hi) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(d));
-}
 template <int V>
 __device__ __forceinline__ void vfma(float (&d)[V], const float (&a)[V], const float (&b)[V], const float (&c)[V]) {
   if constexpr (V == 1) {
@@ -105,9 +97,8 @@ __device__ __forceinline__ void vfma(float (&d)[V], const float (&a)[V], const f
 #pragma unroll
     for (int v = 0; v < V; v += 2) {
       uint64_t r;
-      asm("fma.rn.f32x2 %0, %1, %2, %3;"
-          : "=l"(r) : "l"(pair(a[v], a[v + 1])), "l"(pair(b[v], b[v + 1])), "l"(pair(c[v], c[v + 1])));
-      split(r, d[v], d[v + 1]);
+      r = fma_f32x2(pair_f32(a[v], a[v + 1]), pair_f32(b[v], b[v + 1]), pair_f32(c[v], c[v + 1]));
+      split_f32(r, d[v], d[v + 1]);
     }
   }
 }
@@ -119,8 +110,8 @@ __device__ __forceinline__ void vmul(float (&d)[V], const float (&a)[V], const f
 #pragma unroll
     for (int v = 0; v < V; v += 2) {
       uint64_t r;
-      asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pair(a[v], a[v + 1])), "l"(pair(b[v], b[v + 1])));
-      split(r, d[v], d[v + 1]);
+      asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pair_f32(a[v], a[v + 1])), "l"(pair_f32(b[v], b[v + 1])));
+      split_f32(r, d[v], d[v + 1]);
     }
   }
 }
@@ -132,8 +123,8 @@ __device__ __forceinline__ void vadd(float (&d)[V], const float (&a)[V], const f
 #pragma unroll
     for (int v = 0; v < V; v += 2) {
       uint64_t r;
-      asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pair(a[v], a[v + 1])), "l"(pair(b[v], b[v + 1])));
-      split(r, d[v], d[v + 1]);
+      asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pair_f32(a[v], a[v + 1])), "l"(pair_f32(b[v], b[v + 1])));
+      split_f32(r, d[v], d[v + 1]);
     }
   }
 }
