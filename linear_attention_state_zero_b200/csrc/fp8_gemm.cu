@@ -714,6 +714,13 @@ cudaError_t launch_pair(const GemmFp8Launch &p, unsigned *err_word, cudaStream_t
   return launch_clusters(kern, (unsigned)(2 * pairs), C::THREADS, C::SMEM, 2, s, pdl, args);
 }
 
+// CTAs that split K: as long as the clusters still fit the GPU at once and each keeps two blocks.
+int few_split(int64_t tiles, int kblocks) {
+  int S = 1;
+  while (S < 8 && tiles * S * 2 <= device_sm_count() && kblocks >= 4 * S) S *= 2;
+  return S;
+}
+
 template <int NT>
 cudaError_t launch_few(const GemmFp8Launch &p, unsigned *err_word, cudaStream_t s, bool pdl, std::string *err) {
   using C = FewCfg<NT>;
@@ -725,10 +732,7 @@ cudaError_t launch_few(const GemmFp8Launch &p, unsigned *err_word, cudaStream_t 
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
   if (e != cudaSuccess) return e;
   const int64_t tiles = (int64_t)((p.T + NT - 1) / NT) * ((p.N + BM - 1) / BM);
-  const int kblocks = (p.K + BK - 1) / BK;
-  // split K while the clusters still fit the GPU at once and each CTA keeps two blocks or more
-  int S = 1;
-  while (S < 8 && tiles * S * 2 <= device_sm_count() && kblocks >= 4 * S) S *= 2;
+  const int S = few_split(tiles, (p.K + BK - 1) / BK);
   GemmFp8Launch q = p;
   void *args[] = {&tw, &ta, &q, &err_word};
   return launch_clusters(kern, (unsigned)(tiles * S), kFewThreads, C::SMEM, (unsigned)S, s, pdl, args);
@@ -739,18 +743,23 @@ cudaError_t launch_few(const GemmFp8Launch &p, unsigned *err_word, cudaStream_t 
 cudaError_t launch_gemm_fp8(const GemmFp8Launch &p, unsigned *err_word, cudaStream_t s, bool pdl,
                             std::string *err) {
   if (p.T <= 0 || p.N <= 0) return cudaSuccess;
-  if (p.T <= 16) return launch_few<16>(p, err_word, s, pdl, err);
-  if (p.T <= 32) return launch_few<32>(p, err_word, s, pdl, err);
-  const int64_t few = (int64_t)((p.T + 63) / 64) * ((p.N + BM - 1) / BM);
-  if (p.T <= 64 || few <= device_sm_count()) return launch_few<64>(p, err_word, s, pdl, err);
-  const int pairs = std::max(1, device_sm_count() / 2);
+  // The cycles that a call takes, by rounds of tiles and blocks of K: 350 + 9 NT for a block of
+  // the few-token kernel (measured 500 at 16 tokens, 950 at 64), 510 and 740 for one of the pair
+  // kernel's, and 1500 more for what a pair or a split tile does once.
+  const int sms = device_sm_count(), pairs = std::max(1, sms / 2), kblocks = (p.K + BK - 1) / BK;
+  auto rounds = [](int64_t tiles, int64_t at_once) { return (tiles + at_once - 1) / at_once; };
+  const int nt = p.T <= 16 ? 16 : p.T <= 32 ? 32 : 64;
+  const int64_t few_tiles = (int64_t)((p.T + nt - 1) / nt) * ((p.N + BM - 1) / BM);
+  const int S = few_split(few_tiles, kblocks);
+  const int64_t few = rounds(few_tiles * S, sms) * ((kblocks + S - 1) / S) * (350 + 9 * nt) + (S > 1 ? 1500 : 0);
   const int64_t m = (p.T + 2 * BM - 1) / (2 * BM);
-  const int64_t w128 = (m * ((p.N + 127) / 128) + pairs - 1) / pairs;
-  const int64_t w256 = (m * ((p.N + 255) / 256) + pairs - 1) / pairs;
-  // A block of 128 columns of K takes 740 cycles at BN = 256 and 510 at BN = 128 (4096 x 4736):
-  // the narrow tile only where it needs no more rounds.
-  if (w128 <= w256) return launch_pair<128>(p, err_word, s, pdl, err);
-  return launch_pair<256>(p, err_word, s, pdl, err);
+  const int64_t p128 = rounds(m * ((p.N + 127) / 128), pairs) * kblocks * 510 + 1500;
+  const int64_t p256 = rounds(m * ((p.N + 255) / 256), pairs) * kblocks * 740 + 1500;
+  if (few <= std::min(p128, p256))
+    return nt == 16   ? launch_few<16>(p, err_word, s, pdl, err)
+           : nt == 32 ? launch_few<32>(p, err_word, s, pdl, err)
+                      : launch_few<64>(p, err_word, s, pdl, err);
+  return p128 <= p256 ? launch_pair<128>(p, err_word, s, pdl, err) : launch_pair<256>(p, err_word, s, pdl, err);
 }
 
 }  // namespace tr
