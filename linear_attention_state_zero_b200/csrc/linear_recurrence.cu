@@ -292,7 +292,9 @@ __device__ __forceinline__ void leave(uint32_t S) {
 // where sequences begin in the tokens [t0, t0 + n], n < 31: bit i for a cu entry equal to t0 + i
 // (cu[N] = T among them).  lookup_up starts from a sequence `seq` that begins at or before t0,
 // lookup_down from an entry `top` that is past t0 + n or the last such (and cu[low] <= t0).  The
-// whole warp calls them with the same arguments; one load of 32 entries is the rule.
+// whole warp calls them with the same arguments; one load of 32 entries is the rule.  (Offsets on
+// the device that are not the host's give a wrong result, but neither a walk without end nor a
+// sequence that does not exist.)
 __device__ __forceinline__ uint32_t bits_of(int v, int t0, int n) {
   return v >= t0 && v - t0 <= n ? 1u << (v - t0) : 0u;
 }
@@ -304,10 +306,10 @@ __device__ __forceinline__ uint32_t lookup_up(const int32_t *__restrict__ cu, in
   for (;; at += 31) {
     v = __ldg(cu + (at + lane < n_seqs ? at + lane : n_seqs));
     le = __ballot_sync(0xffffffffu, v <= t0);   // lanes 0 .. k
-    if (le != 0xffffffffu) break;
+    if (le != 0xffffffffu || at >= n_seqs) break;
   }
-  const int k = __popc(le) - 1;
-  seq = at + k;
+  const int k = min(max(__popc(le) - 1, 0), 30);
+  seq = min(at + k, n_seqs - 1);
   from = __shfl_sync(0xffffffffu, v, k);
   to = __shfl_sync(0xffffffffu, v, k + 1);
   uint32_t m = bits_of(v, t0, n);
@@ -327,9 +329,9 @@ __device__ __forceinline__ uint32_t lookup_down(const int32_t *__restrict__ cu, 
     const int v = __ldg(cu + (at + lane < top ? at + lane : top));
     m |= bits_of(v, t0, n);
     const uint32_t le = __ballot_sync(0xffffffffu, v <= t0);
-    if (le) {
-      const int k = __popc(le) - 1;
-      seq = at + k;
+    if (le || at <= low) {
+      const int k = min(max(__popc(le) - 1, 0), 30);
+      seq = min(at + k, max(top - 1, low));
       from = __shfl_sync(0xffffffffu, v, k);
       to = __shfl_sync(0xffffffffu, v, k + 1);
       return __reduce_or_sync(0xffffffffu, m);
@@ -538,7 +540,7 @@ __global__ void __launch_bounds__(kW * 32, 2) recurrence_kernel(RecurrenceLaunch
       for (int i = 0; i < LS; ++i) {
         if (i >= lim) continue;
         if (mask >> i & 1u) {
-          while (__ldg(p.cu + n + 1) <= t0 + i) ++n;
+          while (n + 1 < p.n_seqs && __ldg(p.cu + n + 1) <= t0 + i) ++n;
 #pragma unroll
           for (int v = 0; v < V; ++v)
             B[v] = p.h0 && live ? fmaf(a[i][v], p.h0[(int64_t)n * p.C + c + v], x[i][v]) : x[i][v];
@@ -576,7 +578,7 @@ __global__ void __launch_bounds__(256) recurrence_step_kernel(RecurrenceLaunch p
     const int c = ((int)(b - (int64_t)n * per) * 256 + (int)threadIdx.x) * V;
     if (c >= p.C) continue;
     const int t = __ldg(p.cu + n);
-    const bool some = __ldg(p.cu + n + 1) > t;
+    const bool some = __ldg(p.cu + n + 1) > t && t >= 0 && t < p.T;
     const int64_t hc = (int64_t)n * p.C + c;
     float h[V] = {};
     if (p.h0) to_f32(ld_raw<float, V>(p.h0 + hc), h);

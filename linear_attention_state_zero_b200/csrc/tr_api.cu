@@ -1199,7 +1199,9 @@ tr_status tr_projection_fp8(const uint8_t *a, int64_t a_stride, const float *a_s
   if (n_tokens < 0 || n_tokens > 0x7fffffffLL || n_out <= 0 || n_in <= 0)
     return fail(TR_ERR_INVALID_ARG, "bad sizes");
   if (n_in % 16) return fail(TR_ERR_UNSUPPORTED, "n_in = %d is not a multiple of 16", n_in);
-  if (((n_tokens + 127) / 128) * (((int64_t)n_out + 127) / 128) > 0x7fffffffLL)
+  // (rounded up to whole tiles the sizes stay in 32 bits)
+  if (n_tokens > 0x7ffffe00LL || n_out > 0x7ffffe00 || n_in > 0x7ffffe00 ||
+      ((n_tokens + 127) / 128) * (((int64_t)n_out + 127) / 128) > 0x7fffffffLL)
     return fail(TR_ERR_UNSUPPORTED, "%lld x %d outputs are too many", (long long)n_tokens, n_out);
   if (!known_dtype(y_dtype)) return fail(TR_ERR_DTYPE, "y_dtype");
   if (n_tokens > 0 && (!a || !a_scale || !w || !w_scale || !y))

@@ -142,6 +142,40 @@ def test_projection_fp8(cuda_device, T, N, K, yd):
     assert torch.equal(y, tr.projection_fp8(a, sa, w, sw, out_dtype=yd))   # bitwise
 
 
+# tiles of 256 and of 128 columns, several to a pair of CTAs, K of odd numbers of blocks and of
+# several sets of scales; few tokens with K whole and split; rows of y that are and are not
+# 16-byte aligned
+@pytest.mark.parametrize("T,N,K,yd", [
+    (1300, 3000, 640, BF), (1300, 3001, 2208, F32), (1300, 3004, 2208, F32), (2600, 4104, 2176, BF),
+    (3300, 5000, 144, F32), (520, 9000, 400, BF), (300, 1200, 1040, F32),
+    (2, 9500, 4240, BF), (40, 9700, 160, F32), (33, 500, 4112, BF), (64, 130, 3200, F32), (12, 2500, 384, BF),
+])
+def test_projection_fp8_tiles(cuda_device, T, N, K, yd):
+    a, sa = operand(T, K, 17 + T, 1, cuda_device)
+    w, sw = operand(N, K, 18 + N, 128, cuda_device, 0.02)
+    y = tr.projection_fp8(a, sa, w, sw, out_dtype=yd)
+    tr.check()
+    rows = torch.arange(T) if T <= 64 else torch.cat([torch.arange(3), torch.randperm(T)[:60], torch.arange(T - 3, T)])
+    check_product(y[rows], a[rows], sa[rows], w, sw)
+    assert torch.equal(y, tr.projection_fp8(a, sa, w, sw, out_dtype=yd))
+
+
+@pytest.mark.parametrize("yd", [BF, F32])
+@pytest.mark.parametrize("T,N,at", [(700, 4100, 16), (1500, 2904, 8), (1500, 2904, 9), (60, 300, 8)])
+def test_projection_fp8_into_a_slice(cuda_device, T, N, at, yd):
+    """y as a slice of a wider matrix, at a 16-byte aligned column and not: rows and columns
+    beside it stay as they were."""
+    a, sa = operand(T, 384, 3, 1, cuda_device)
+    w, sw = operand(N, 384, 4, 128, cuda_device, 0.05)
+    out = torch.full((T + 2, N + 24), 7.0, dtype=yd, device=cuda_device)
+    y = tr.projection_fp8(a, sa, w, sw, y=out[1:T + 1, at:at + N])
+    tr.check()
+    check_product(y, a, sa, w, sw)
+    keep = torch.ones_like(out, dtype=torch.bool)
+    keep[1:T + 1, at:at + N] = False
+    assert (out[keep] == 7).all()
+
+
 @pytest.mark.parametrize("yd", [BF, F32])
 @pytest.mark.parametrize("T", [5, 200, 600])
 def test_projection_fp8_strided(cuda_device, T, yd):

@@ -225,6 +225,86 @@ def test_large_calls_on_sampled_channels(cuda_device, lengths, C):
         near(grads[k][:, at], w[k], w[3 + k])
 
 
+# the widths of every vector of channels (4, 2 and 1 a lane) and tile; one long sequence, a few and
+# many, unbalanced ones, empty ones by the hundred between the others
+SPREADS = [
+    ([9000], 2048, F32, F32), ([9000], 256, BF, F32), ([6000], 1024, BF, BF), ([5000], 98, F32, BF), ([7000], 301, BF, BF),
+    ([3000, 100, 1, 5000], 2022, F32, F32), ([3000, 0, 2500], 1023, F32, BF), ([200] * 70, 512, BF, F32),
+    ([0] * 100 + [5] + [0] * 70 + [300] + [1] * 200 + [0] * 40 + [2000] + [0] * 50, 260, BF, BF),
+    ([3] * 400 + [1500] + [2] * 300, 129, BF, BF), ([900, 17] * 40, 4096, F32, F32), ([1200] * 8, 1028, BF, BF),
+]
+
+
+@pytest.mark.parametrize("states", [False, True])
+@pytest.mark.parametrize("case", range(len(SPREADS)))
+def test_spreads_on_sampled_channels(cuda_device, case, states):
+    lengths, C, xd, gd = SPREADS[case]
+    cu, T, N, logits = offsets(lengths), sum(lengths), len(lengths), (case + states) % 2 == 0
+    gen = torch.Generator(device=cuda_device)
+    gen.manual_seed(case)
+    rn = lambda *s: torch.randn(s, generator=gen, device=cuda_device)  # noqa: E731
+    g = rn(T, C) - 3
+    x, g, dy = rn(T, C).to(xd), (g if logits else -torch.nn.functional.softplus(g)).to(gd), rn(T, C).to(xd)
+    h0, dh = (rn(N, C), rn(N, C)) if states else (None, None)
+    y, fin = tr.linear_recurrence(x, g, cu, h0=h0, gate_logits=logits)
+    grads = tr.linear_recurrence_backward(dy, g, y, cu, h0=h0, dh_final=dh, gate_logits=logits, want_dh0=True)
+    tr.check()
+    again = tr.linear_recurrence(x, g, cu, h0=h0, gate_logits=logits) + tr.linear_recurrence_backward(
+        dy, g, y, cu, h0=h0, dh_final=dh, gate_logits=logits, want_dh0=True)
+    assert all(torch.equal(a, b) for a, b in zip((y, fin) + grads, again))
+    at = sorted({0, 1, 2, 3, C // 2, C // 3, C - 2, C - 1})
+    part = lambda t: None if t is None else f64(t[:, at])  # noqa: E731
+    w = ref.recurrence(part(x), part(g), cu, part(h0), logits)
+    near(y[:, at], w[0], w[2])
+    near(fin[:, at], w[1], w[3])
+    w = ref.recurrence_grad(part(dy), part(g), part(y), cu, part(h0), part(dh), logits)
+    for k in range(3):
+        near(grads[k][:, at], w[k], w[3 + k])
+
+
+@pytest.mark.parametrize("xd,gd", [(BF, BF), (BF, F32), (F32, BF), (F32, F32)])
+@pytest.mark.parametrize("C,at", [(7, 0), (8, 0), (1028, 0), (1028, 2), (4096, 4), (300, 1)])
+def test_single_tokens(cuda_device, C, at, xd, gd):
+    """Sequences of one token or none: with and without states, in place, into and from slices."""
+    lengths = [1, 0, 1, 1, 0, 0, 1, 1, 1]
+    cu, T, N = offsets(lengths), sum(lengths), len(lengths)
+    x, g, h0 = rnd((T, C), 1, xd), gates((T, C), 2, gd, True), rnd((N, C), 3)
+    xw = torch.zeros((T, C + 12), dtype=xd)
+    xw[:, at:at + C] = x
+    gw = torch.zeros((T, C + 8), dtype=gd)
+    gw[:, at:at + C] = g
+    out = torch.full((T, C + 16), 7.0, dtype=xd, device=cuda_device)
+    xs, gs = xw.to(cuda_device)[:, at:at + C], gw.to(cuda_device)[:, at:at + C]
+    for start in (None, h0):
+        wy, wf, by, bf = ref.recurrence(f64(x), f64(g), cu, None if start is None else f64(start), True)
+        h = None if start is None else start.to(cuda_device)
+        y, fin = tr.linear_recurrence(xs, gs, cu, h0=h, gate_logits=True, y=out[:, at:at + C], h_final=h)
+        near(y, wy, by)
+        near(fin, wf, bf)
+        assert (out[:, :at] == 7).all() and (out[:, at + C:] == 7).all()
+        none, fin2 = tr.linear_recurrence(xs, gs, cu, h0=None if start is None else start.to(cuda_device),
+                                          gate_logits=True, want_y=False)
+        assert none is None and torch.equal(fin, fin2)
+
+
+def test_infinite_states_stay_in_their_sequence(cuda_device):
+    """An infinite final state and gates that forget everything next to it, over several rounds."""
+    lengths, C = [1500, 700, 2000], 66
+    cu, T = offsets(lengths), sum(lengths)
+    x, g = rnd((T, C), 1).to(cuda_device), gates((T, C), 2, F32, True).to(cuda_device)
+    y, fin = tr.linear_recurrence(x, g, cu, gate_logits=True)
+    h0 = torch.zeros((3, C), device=cuda_device)
+    h0[0] = float("inf")
+    y2, fin2 = tr.linear_recurrence(x, g, cu, h0=h0, gate_logits=True)
+    assert torch.isinf(y2[:1500]).all() and torch.equal(y2[1500:], y[1500:]) and torch.equal(fin2[1:], fin[1:])
+    dh = torch.zeros((3, C), device=cuda_device)
+    back = tr.linear_recurrence_backward(x, g, y, cu, dh_final=dh, gate_logits=True, want_dh0=True)
+    dh[2] = float("inf")
+    back2 = tr.linear_recurrence_backward(x, g, y, cu, dh_final=dh, gate_logits=True, want_dh0=True)
+    assert torch.isinf(back2[0][2200:]).all()
+    assert all(torch.equal(a[:2200], b[:2200]) for a, b in zip(back[:2], back2[:2])) and torch.equal(back[2][:2], back2[2][:2])
+
+
 def test_other_stream_and_graph(cuda_device):
     cu = tr.seqlens(offsets([300, 0, 41, 800]), cuda_device)
     x, g = rnd((1141, 96), 1).to(cuda_device), gates((1141, 96), 2, F32, False).to(cuda_device)

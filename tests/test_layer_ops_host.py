@@ -123,6 +123,11 @@ def test_projection_refusals(kw, status):
     assert _proj(**kw) == status, tr.lib.tr_last_error()
 
 
+@pytest.mark.parametrize("kw", [dict(t=0x7fffffff), dict(n=0x7fffffff), dict(k=0x7ffffff0)])
+def test_projection_sizes_that_pass_32_bits_in_whole_tiles(kw):
+    assert _proj(**kw) == 5
+
+
 def test_projection_of_no_token_needs_no_device():
     assert _proj(t=0, a=None, sa=None, y=None) == 0
 
