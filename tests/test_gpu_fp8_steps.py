@@ -205,6 +205,27 @@ def test_projection_fp8_nan_stays_in_its_row_and_column(cuda_device, T):
     assert np.isnan(y[bad]).all() and np.isfinite(y[~bad]).all()
 
 
+def test_offsets_past_32_bits(cuda_device):
+    """More than 2^31 elements in and out: the last rows against fp64."""
+    T, D, N = 530000, 4096, 4112
+    gen = torch.Generator(device=cuda_device)
+    gen.manual_seed(1)
+    x = torch.empty((T, D), dtype=BF, device=cuda_device).normal_(generator=gen)
+    q, s, out = tr.rmsnorm_fp8(x, residual=x)
+    n, total = ref.rmsnorm(f64(x[-40:]), f64(x[-40:]))
+    check_quantized(q[-40:], s[-40:], n, 1, 2.0 ** -18)
+    assert (np.abs(f64(out[-40:]) - total) <= (HALF[BF] + 2.0 ** -24) * np.abs(total)).all()
+    check_quantized(*(t[-40:] for t in tr.quantize_fp8(x)), f64(x[-40:]), 1, 2.0 ** -23)
+    tq, ts = tr.quantize_fp8(x, block_rows=128)
+    last = T // 128 * 128
+    check_quantized(tq[last:], ts[last // 128:], f64(x[last:]), 128, 2.0 ** -23)
+    w, sw = operand(N, 128, 2, 128, cuda_device)
+    a, sa = q[:, :128], s[:, :1].contiguous()
+    y = tr.projection_fp8(a, sa, w, sw)
+    tr.check()
+    check_product(y[-40:], a[-40:], sa[-40:], w, sw)
+
+
 def test_no_rows(cuda_device):
     x = torch.empty((0, 256), device=cuda_device)
     q, s, out = tr.rmsnorm_fp8(x, residual=x)

@@ -305,6 +305,46 @@ def test_infinite_states_stay_in_their_sequence(cuda_device):
     assert all(torch.equal(a[:2200], b[:2200]) for a, b in zip(back[:2], back2[:2])) and torch.equal(back[2][:2], back2[2][:2])
 
 
+def test_offsets_past_32_bits(cuda_device):
+    """More than 2^31 elements: the last, short sequence against fp64, forward and backward."""
+    lengths, C, gen = [530000, 900], 4096, torch.Generator(device=cuda_device)
+    cu, T = offsets(lengths), sum(lengths)
+    gen.manual_seed(1)
+    x = torch.empty((T, C), dtype=BF, device=cuda_device).normal_(generator=gen)
+    g = torch.empty((T, C), dtype=BF, device=cuda_device).normal_(-3, 1, generator=gen)
+    y, fin = tr.linear_recurrence(x, g, cu, gate_logits=True)
+    dx, dg, _ = tr.linear_recurrence_backward(x, g, y, cu, gate_logits=True)
+    tr.check()
+    at, n = [0, 1, 2047, C - 1], lengths[1]
+    w = ref.recurrence(f64(x[-n:, at]), f64(g[-n:, at]), [0, n], None, True)
+    near(y[-n:, at], w[0], w[2])
+    near(fin[1:, at], w[1], w[3])
+    w = ref.recurrence_grad(f64(x[-n:, at]), f64(g[-n:, at]), f64(y[-n:, at]), [0, n], None, None, True)
+    near(dx[-n:, at], w[0], w[3])
+    near(dg[-n:, at], w[1], w[4])
+
+
+def test_two_calls_at_once(cuda_device):
+    """Calls on two streams, clusters among them, interleaved: each is what it is alone."""
+    sets = []
+    for lengths, C in (([9000], 256), ([400] * 30, 512)):
+        T = sum(lengths)
+        x, g = rnd((T, C), C, BF).to(cuda_device), gates((T, C), 2, BF, True).to(cuda_device)
+        sets.append((x, g, tr.seqlens(offsets(lengths), cuda_device)))
+    want = [tr.linear_recurrence(x, g, cu, gate_logits=True) for x, g, cu in sets]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(5):
+        for k, (x, g, cu) in enumerate(sets):
+            got[k].append(tr.linear_recurrence(x, g, cu, gate_logits=True, stream=streams[k]))
+    torch.cuda.synchronize()
+    tr.check()
+    for k in range(2):
+        for y, fin in got[k]:
+            assert torch.equal(y, want[k][0]) and torch.equal(fin, want[k][1])
+
+
 def test_other_stream_and_graph(cuda_device):
     cu = tr.seqlens(offsets([300, 0, 41, 800]), cuda_device)
     x, g = rnd((1141, 96), 1).to(cuda_device), gates((1141, 96), 2, F32, False).to(cuda_device)
