@@ -14,9 +14,9 @@
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
+#include "fp8_ptx.cuh"
 #include "layer_ops.h"
 #include "tr_internal.h"
-#include "tr_ptx.cuh"
 
 namespace tr {
 namespace {
@@ -75,26 +75,48 @@ __device__ __forceinline__ void store8(void *p, int64_t off, const float (&f)[8]
   }
 }
 
-__device__ __forceinline__ float abs_max8(const float (&f)[8]) {
-  float m = 0.f;
+// The largest magnitude of 8 elements as the bits of an fp32: magnitudes order like their bits
+// as unsigned integers, with a NaN above infinity, so that the largest is NaN if any is.
+__device__ __forceinline__ uint32_t abs_max8(const float (&f)[8]) {
+  uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m = max_nan(m, fabsf(f[i]));
+  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(f[i]) & 0x7fffffffu);
+  return m;
+}
+__device__ __forceinline__ uint32_t abs_max8(const Raw8<true> &r) {   // two at a time
+  const uint32_t w[4] = {r.u.x, r.u.y, r.u.z, r.u.w};
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) asm("max.u16x2 %0, %1, %2;" : "=r"(m) : "r"(m), "r"(w[i] & 0x7fff7fffu));
+  return max(m & 0xffff0000u, m << 16);
+}
+__device__ __forceinline__ uint32_t abs_max8(const Raw8<false> &r) {
+  float f[8];
+  r.to_f32(f);
+  return abs_max8(f);
+}
+// Over the 16 lanes that share a scale block.
+__device__ __forceinline__ uint32_t max_of_16(uint32_t m) {
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
   return m;
 }
 
 // The scale of a block whose largest magnitude is m.
-__device__ __forceinline__ float scale_of(float m) {
-  return max_nan(__fdiv_rn(m, 448.f), 1.17549435e-38f);
+__device__ __forceinline__ float scale_of(uint32_t m) {
+  return max_nan(__fdiv_rn(__uint_as_float(m), 448.f), 1.17549435e-38f);
 }
 
 __device__ __forceinline__ void store_q8(uint8_t *dst, const float (&f)[8], float inv) {
   uint32_t w[2];
+  const uint64_t ii = pair_f32(inv, inv);
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(f[4 * h] * inv, f[4 * h + 1] * inv),
-                                                 __NV_SATFINITE, __NV_E4M3);
-    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(f[4 * h + 2] * inv, f[4 * h + 3] * inv),
-                                                 __NV_SATFINITE, __NV_E4M3);
+    float a, b, c, d;
+    split_f32(mul_f32x2(pair_f32(f[4 * h], f[4 * h + 1]), ii), a, b);
+    split_f32(mul_f32x2(pair_f32(f[4 * h + 2], f[4 * h + 3]), ii), c, d);
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
     w[h] = lo | (hi << 16);
   }
   *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
@@ -156,7 +178,7 @@ __global__ void __launch_bounds__(WPR < 8 ? 256 : WPR * 32)
   }
   const float rms = rsqrtf(ss / (float)p.D + p.eps);
   const int kb = (p.D + kScaleBlock - 1) / kScaleBlock;
-  float mine = 0.f;
+  uint32_t mine = 0;
 #pragma unroll
   for (int j = 0; j < kNV; ++j) {
     const int c = first(j) + lane * 8;
@@ -169,9 +191,7 @@ __global__ void __launch_bounds__(WPR < 8 ? 256 : WPR * 32)
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) f[j][i] = f[j][i] * rms * g[i];
-    float m = abs_max8(f[j]);
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const uint32_t m = max_of_16(abs_max8(f[j]));
     if (lane % kNV == j) mine = m;
   }
   const float my_scale = scale_of(mine), my_inv = __frcp_rn(my_scale);
@@ -203,22 +223,17 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(QuantFp8Launch p) {
   pdl_trigger();
   pdl_wait();
   if (row >= p.rows) return;
-  float f[kNV][8], m[kNV];
+  Raw8<XBF> raw[kNV];
 #pragma unroll
   for (int j = 0; j < kNV; ++j) {
-    if (c0 + 256 * j < p.cols) load8<XBF>(p.x, row * p.x_stride + c0 + 256 * j, f[j]);
-    else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) f[j][i] = 0.f;
-    }
+    raw[j] = Raw8<XBF>{};
+    if (c0 + 256 * j < p.cols) raw[j].load(p.x, row * p.x_stride + c0 + 256 * j);
   }
-  float mine = 0.f;
+  uint32_t mine = 0;
 #pragma unroll
   for (int j = 0; j < kNV; ++j) {
-    m[j] = abs_max8(f[j]);
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) m[j] = max_nan(m[j], __shfl_xor_sync(0xffffffffu, m[j], o));
-    if (lane % kNV == j) mine = m[j];
+    const uint32_t m = max_of_16(abs_max8(raw[j]));
+    if (lane % kNV == j) mine = m;
   }
   const float my_scale = scale_of(mine), my_inv = __frcp_rn(my_scale);
 #pragma unroll
@@ -227,7 +242,9 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(QuantFp8Launch p) {
     const float inv = __shfl_sync(0xffffffffu, my_inv, (lane & 16) + j);
     const int c = c0 + 256 * j;
     if (c < p.cols) {
-      store_q8(p.q + row * p.cols + c, f[j], inv);
+      float f[8];
+      raw[j].to_f32(f);
+      store_q8(p.q + row * p.cols + c, f, inv);
       if ((lane & 15) == 0) p.scale[row * kb + c / kScaleBlock] = s;
     }
   }
@@ -237,7 +254,7 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(QuantFp8Launch p) {
 // thread (16 lanes across the columns, 16 row groups).
 template <bool XBF>
 __global__ void __launch_bounds__(256) quantize_tile_kernel(QuantFp8Launch p) {
-  __shared__ float part[8];
+  __shared__ uint32_t part[8];
   const int kb = (p.cols + kScaleBlock - 1) / kScaleBlock;
   const int64_t rb = blockIdx.x / kb;
   const int cb = (int)(blockIdx.x - rb * kb);
@@ -251,19 +268,14 @@ __global__ void __launch_bounds__(256) quantize_tile_kernel(QuantFp8Launch p) {
     raw[j] = Raw8<XBF>{};
     if (r0 + 16 * j < p.rows && c < p.cols) raw[j].load(p.x, (r0 + 16 * j) * p.x_stride + c);
   }
-  float m = 0.f;
+  uint32_t m = 0;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    float f[8];
-    raw[j].to_f32(f);
-    m = max_nan(m, abs_max8(f));
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+  for (int j = 0; j < 8; ++j) m = max(m, abs_max8(raw[j]));
+  m = __reduce_max_sync(0xffffffffu, m);
   if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < 8; ++w) m = max_nan(m, part[w]);
+  for (int w = 0; w < 8; ++w) m = max(m, part[w]);
   const float s = scale_of(m);
   const float inv = __frcp_rn(s);
 #pragma unroll

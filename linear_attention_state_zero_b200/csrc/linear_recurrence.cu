@@ -96,8 +96,7 @@ __device__ __forceinline__ void vfma(float (&d)[V], const float (&a)[V], const f
   } else {
 #pragma unroll
     for (int v = 0; v < V; v += 2) {
-      uint64_t r;
-      r = fma_f32x2(pair_f32(a[v], a[v + 1]), pair_f32(b[v], b[v + 1]), pair_f32(c[v], c[v + 1]));
+      const uint64_t r = fma_f32x2(pair_f32(a[v], a[v + 1]), pair_f32(b[v], b[v + 1]), pair_f32(c[v], c[v + 1]));
       split_f32(r, d[v], d[v + 1]);
     }
   }
@@ -109,8 +108,7 @@ __device__ __forceinline__ void vmul(float (&d)[V], const float (&a)[V], const f
   } else {
 #pragma unroll
     for (int v = 0; v < V; v += 2) {
-      uint64_t r;
-      asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pair_f32(a[v], a[v + 1])), "l"(pair_f32(b[v], b[v + 1])));
+      const uint64_t r = mul_f32x2(pair_f32(a[v], a[v + 1]), pair_f32(b[v], b[v + 1]));
       split_f32(r, d[v], d[v + 1]);
     }
   }
