@@ -641,7 +641,7 @@ __global__ void __launch_bounds__(kW * 32, 2) recurrence_grad_kernel(RecurrenceG
 #pragma unroll 1
   for (int i = 0; i < STAGES - 1; ++i) fetch(i);
   if (parts.some_empty && p.dh0)
-    copy_empty<V>(p.cu, p.n_seqs, (int)((blockIdx.y * S + r) * kW) + warp, (int)(gridDim.y * S * kW),
+    copy_empty<V>(p.cu, p.n_seqs, (int)((blockIdx.y * S + r) * SEGS) + seg, (int)(gridDim.y * S * SEGS),
                   c, live, p.C, p.dh_final, p.dh0);
 #pragma unroll 1
   for (int tr1 = te - 1; tr1 >= tb;
@@ -673,6 +673,19 @@ __global__ void __launch_bounds__(kW * 32, 2) recurrence_grad_kernel(RecurrenceG
     const uint32_t rev = lim > 0 ? __brev(mask) >> (31 - lim) : 0u;  // bit j: t0 + lim - j starts
     const uint32_t ends = rev & ((1u << (lim > 0 ? lim : 0)) - 1u);
     const uint32_t begins = rev >> 1;
+    // The states of the first of each (h0 and dh_final are read in front of the wait for the
+    // segment's own data; a segment that holds more of them reads the others where it needs them).
+    const int b1 = begins ? __ffs(begins) - 1 : -1, e1 = ends ? __ffs(ends) - 1 : -1;
+    float hb[V], he[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) hb[v] = he[v] = 0.f;
+    auto state = [&](const float *from, int i, float (&h)[V]) {   // of token t1 - i's sequence
+      const int64_t at = (int64_t)seq_of(t1 - i) * p.C + c;
+#pragma unroll
+      for (int v = 0; v < V; ++v) h[v] = from && live ? from[at + v] : 0.f;
+    };
+    if (b1 >= 0 && p.h0) state(p.h0, b1, hb);
+    if (e1 >= 0 && p.dh_final) state(p.dh_final, e1, he);
     fetch(stage == 0 ? STAGES - 1 : stage - 1);   // into the slots of the round before
     cp_wait<STAGES - 1>();
     float a[LS][V], d[LS][V], q[LS][V];   // q = h_{t-1} d(log a)/d(gate)
@@ -683,9 +696,9 @@ __global__ void __launch_bounds__(kW * 32, 2) recurrence_grad_kernel(RecurrenceG
       to_f32(rh.get(stage, i), h);
       to_f32(rg.get(stage, i), g);
       if (begins >> i & 1u) {
-        const int n = seq_of(t1 - i);
+        if (i != b1) state(p.h0, i, hb);
 #pragma unroll
-        for (int v = 0; v < V; ++v) h[v] = p.h0 && live ? p.h0[(int64_t)n * p.C + c + v] : 0.f;
+        for (int v = 0; v < V; ++v) h[v] = hb[v];
       }
       decay<LOGITS, true>(g, a[i], h, q[i]);
     }
@@ -734,10 +747,9 @@ __global__ void __launch_bounds__(kW * 32, 2) recurrence_grad_kernel(RecurrenceG
           continue;
         }
         if (ends >> i & 1u) {
-          const int n = seq_of(t1 - i);
+          if (i != e1) state(p.dh_final, i, he);
 #pragma unroll
-          for (int v = 0; v < V; ++v)
-            B[v] = p.dh_final && live ? p.dh_final[(int64_t)n * p.C + c + v] : 0.f;
+          for (int v = 0; v < V; ++v) B[v] = he[v];
         }
         emit(i, B);
         put_first(i, B);
