@@ -415,6 +415,15 @@ __device__ __forceinline__ bool all_of(bool b) {
   return G == 1 ? b : __all_sync(0xffffffffu, b);
 }
 
+// V channels of a state (4-byte aligned)
+template <int V>
+__device__ __forceinline__ Raw<float, V> ld_state(const float *p) {
+  Raw<float, V> r;
+#pragma unroll
+  for (int v = 0; v < V; ++v) r.f[v] = p[v];
+  return r;
+}
+
 // Sequences without a token keep their state: to[n] = from[n] (or 0), spread over the warps
 // that own the channels.
 template <int V>
@@ -476,16 +485,6 @@ __global__ void __launch_bounds__(kW * 32, 2) recurrence_kernel(RecurrenceLaunch
 #pragma unroll 1
   for (int tr0 = tb; tr0 < te; tr0 += chunk, t0 += chunk, py += chunk * p.y_stride, ++round) {
     const int lim = te - t0 < LS ? te - t0 : LS;    // tokens of the segment (may be <= 0)
-    fetch(stage == 0 ? STAGES - 1 : stage - 1);   // into the slots of the round before
-    cp_wait<STAGES - 1>();
-    float a[LS][V], x[LS][V];
-#pragma unroll
-    for (int i = 0; i < LS; ++i) {
-      float g[V];
-      to_f32(rg.get(stage, i), g);
-      to_f32(rx.get(stage, i), x[i]);
-      decay<LOGITS>(g, a[i]);
-    }
     uint32_t mask = 0;
     const bool look = lim > 0 && (t0 <= from || t0 + LS >= to);
 #pragma unroll
@@ -499,6 +498,31 @@ __global__ void __launch_bounds__(kW * 32, 2) recurrence_kernel(RecurrenceLaunch
         from = f;
         to = t;
       }
+    }
+    // the state that the segment's first sequence start begins from, read in front of the wait
+    // for the segment's own data (the other starts' are read where they are needed)
+    const uint32_t inside = mask & ((1u << (lim > 0 ? lim : 0)) - 1u);
+    const int first = inside ? __ffs(inside) - 1 : lim;   // tokens of the sequence before
+    auto seq_of = [&](int t) {   // the sequence that holds token t >= t0
+      int n = seq;
+      while (n + 1 < p.n_seqs && __ldg(p.cu + n + 1) <= t) ++n;
+      return n;
+    };
+    int n1 = 0;
+    float hb[V] = {};
+    if (inside) {
+      n1 = seq_of(t0 + first);
+      if (p.h0 && live) to_f32(ld_state<V>(p.h0 + (int64_t)n1 * p.C + c), hb);
+    }
+    fetch(stage == 0 ? STAGES - 1 : stage - 1);   // into the slots of the round before
+    cp_wait<STAGES - 1>();
+    float a[LS][V], x[LS][V];
+#pragma unroll
+    for (int i = 0; i < LS; ++i) {
+      float g[V];
+      to_f32(rg.get(stage, i), g);
+      to_f32(rx.get(stage, i), x[i]);
+      decay<LOGITS>(g, a[i]);
     }
     const bool whole = lim == LS && (mask & ~(1u << LS)) == 0;   // of one sequence, begun before
     float A[V], B[V], u[V];
@@ -529,19 +553,19 @@ __global__ void __launch_bounds__(kW * 32, 2) recurrence_kernel(RecurrenceLaunch
       }
       if (mask >> LS) put_final(seq, u);
     } else {
-      const uint32_t inside = mask & ((1u << (lim > 0 ? lim : 0)) - 1u);
-      const int first = inside ? __ffs(inside) - 1 : lim;   // tokens of the sequence before
       // from the first sequence start on, the states do not depend on what lies before the
       // segment: they are final here
-      int n = seq;
+      int n = n1;
 #pragma unroll
       for (int i = 0; i < LS; ++i) {
         if (i >= lim) continue;
         if (mask >> i & 1u) {
-          while (n + 1 < p.n_seqs && __ldg(p.cu + n + 1) <= t0 + i) ++n;
+          if (i != first) {
+            n = seq_of(t0 + i);
+            if (p.h0 && live) to_f32(ld_state<V>(p.h0 + (int64_t)n * p.C + c), hb);
+          }
 #pragma unroll
-          for (int v = 0; v < V; ++v)
-            B[v] = p.h0 && live ? fmaf(a[i][v], p.h0[(int64_t)n * p.C + c + v], x[i][v]) : x[i][v];
+          for (int v = 0; v < V; ++v) B[v] = p.h0 ? fmaf(a[i][v], hb[v], x[i][v]) : x[i][v];
         } else {
           vfma(B, a[i], B, x[i]);
           vmul(A, A, a[i]);
