@@ -13,12 +13,11 @@
 // gemm_fp8_pair_kernel, for many outputs: a pair of CTAs shares a 256 x BN tile
 // (tcgen05.mma.cta_group::2), so that a block of 128 columns costs each SM (128 + BN / 2) x 128
 // bytes of operands for 128 x BN outputs.  What bounds it is the epilogue: every block is read
-// back from TMEM and added in fp32 registers, 256 cycles of the FMA pipe at BN = 256, and with two
-// buffers of TMEM the way from a buffer's last read over both CTAs' barriers to its next sums is
-// not hidden: a block takes 740 cycles against 512 of the tensor core's (510 at BN = 128).  At 13112 x 12352 x 4096 a call takes
-// 0.71-0.88 ms (1.9-1.5 PFLOP/s, by how far the power limit lowers the clock); a library product
-// with one scale for everything takes 0.47-0.55 ms there.  The first version, tiles of 128 x 128
-// of single CTAs whose products one lane issued, took 1.14 ms.
+// back from TMEM and added in fp32 registers, and a block takes 740 cycles at BN = 256 against
+// 512 of the tensor core's (510 at BN = 128); alone, without products or copies, the epilogue
+// takes 700.  At 13112 x 12352 x 4096 a call takes 0.68 ms (1.9 PFLOP/s, at the power limit); a
+// library product with one scale for everything takes 0.47-0.55 ms there.  The first version,
+// tiles of 128 x 128 of single CTAs whose products one lane issued, took 1.14 ms.
 // gemm_fp8_few_kernel, for few tokens: the weight's rows take the tensor core's M side, and a
 // cluster splits K, so that a small product uses many SMs (8 x 6176 x 2048: 6.4 us).
 #include <cuda_bf16.h>
