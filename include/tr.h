@@ -470,6 +470,8 @@ tr_status tr_projection_fp8(const uint8_t *a, int64_t a_stride, const float *a_s
  * No workspace; may be captured into a graph after one uncaptured call on the device (a replay
  * reads cu_seqlens again, but its spread over the GPU is the captured call's: keep the same
  * offsets).
+ * The waits of a launch that spreads a sequence over a cluster are bounded (TR_ERR_TIMEOUT at
+ * tr_check).  cu_seqlens that differ from cu_seqlens_host give an undefined result.
  */
 enum { TR_GATE_LOGITS = 512u };  /* tr_linear_recurrence(_backward): the gate is a logit */
 

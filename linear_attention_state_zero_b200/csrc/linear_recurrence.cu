@@ -11,11 +11,18 @@
 // in a round each warp (or each of G groups of its lanes) holds a segment of consecutive tokens
 // of its lanes' channels in registers (the next rounds' loads already in flight), reduces it to
 // one map (A, B) per channel, and the segments are joined in time order: those of a CTA through
-// shared memory, the CTAs of the cluster through each other's shared memory (stores that count their
-// bytes on the receiver's mbarrier; a cluster barrier in each round, whose release waits for
-// the loads and stores in flight, took twice as long).  Every lane then knows the state in front of its segment and replays the segment
-// from registers.  Nothing is read twice, nothing passes through global memory, and the order
-// of every sum is fixed, so results are bitwise reproducible.
+// shared memory, the CTAs of the cluster through each other's shared memory (stores that count
+// their bytes on the receiver's mbarrier; a cluster barrier in each round, whose release waits
+// for the loads and stores in flight, took half as long again).  Every lane then knows the state
+// in front of its segment and replays the segment from registers.  Nothing is read twice, nothing
+// passes through global memory, and the order of every sum is fixed, so results are bitwise
+// reproducible.
+//
+// HBM bounds it where the runs of sequences fill the GPU: 65536 x 4096 bf16 in 64 sequences takes
+// 255 us (96% of the measured copy rate), backward 16384 x 4096 fp32 in 40 sequences 209 us (98%).
+// One long sequence is bound by the join of its cluster each round (backward 32768 x 2048, bf16
+// with fp32 gates: 230 us, 62%), a few thousand tokens by the latency of a few rounds of about
+// 2 us, and rows that are not 4-byte (bf16) or 8-byte (fp32) aligned by one channel a lane (35-70%).
 //
 // The packed tokens are scanned as one long sequence that starts over where a sequence
 // begins.  That is a selection, not a product with a = 0, so infinities or NaN of one
