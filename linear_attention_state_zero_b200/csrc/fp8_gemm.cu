@@ -636,7 +636,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       const uint32_t mine = smem_u32(part) + (uint32_t)((r * per * BM + nl) * 4);
 #pragma unroll
       for (int i = 0; i < NT; ++i)
-        if (t0 + i < p.T) st_cluster(cluster_map(mine + (uint32_t)((i & (per - 1)) * BM * 4), (uint32_t)(i >> lg)), acc[i]);
+        if (t0 + i < p.T)
+          st_cluster(cluster_map(mine + (uint32_t)((i & (per - 1)) * BM * 4), (uint32_t)(i >> lg)), acc[i]);
     }
     __syncwarp();
     cluster_sync_all();

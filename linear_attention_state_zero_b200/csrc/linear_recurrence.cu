@@ -686,7 +686,8 @@ __global__ void __launch_bounds__(kW * 32, 2) recurrence_grad_kernel(RecurrenceG
     for (int g = 0; g < G; ++g) {
       if (!of_group<G>(look, g)) continue;
       int sq, f, t;
-      const uint32_t m = lookup_down(p.cu, low, of_group<G>(seq, g) + 1, of_group<G>(t0, g), of_group<G>(lim, g), sq, f, t);
+      const uint32_t m = lookup_down(p.cu, low, of_group<G>(seq, g) + 1, of_group<G>(t0, g),
+                                     of_group<G>(lim, g), sq, f, t);
       if (grp == g) {
         mask = m;
         seq = sq;
@@ -908,14 +909,15 @@ cudaError_t go(const RecurrenceLaunch &p, cudaStream_t s, bool pdl) {
   // bf16 and fp32 gates: 87 us; two in tiles of 64: 103); narrower tiles where those would be too
   // few or would need a cluster (16384 x 4096 in one sequence, fp32: 178 us, 147 with two channels
   // a lane; 65536 x 1024 in one sequence, bf16: 229 us in tiles of 64, 153 in tiles of 32).
+  constexpr int LS4 = kElems / 4, LS2 = kElems / 2;
   cudaError_t e = cudaSuccess;
-  if (fits(4) && choose<4, kElems / 4, 1>(recurrence_kernel<TX, TG, LOGITS, 4, kElems / 4, 1>, p, kTok, true, false, s, pdl, &e))
+  if (fits(4) &&
+      choose<4, LS4, 1>(recurrence_kernel<TX, TG, LOGITS, 4, LS4, 1>, p, kTok, true, false, s, pdl, &e))
     return e;
-  if (!fits(2)) {
+  if (!fits(2))
     choose<1, 16, 1>(recurrence_kernel<TX, TG, LOGITS, 1, 16, 1>, p, kTok, false, true, s, pdl, &e);
-  } else if (!choose<2, kElems / 2, 1>(recurrence_kernel<TX, TG, LOGITS, 2, kElems / 2, 1>, p, kTok, false, false, s, pdl, &e)) {
-    choose<2, kElems / 2, 2>(recurrence_kernel<TX, TG, LOGITS, 2, kElems / 2, 2>, p, kTok, false, true, s, pdl, &e);
-  }
+  else if (!choose<2, LS2, 1>(recurrence_kernel<TX, TG, LOGITS, 2, LS2, 1>, p, kTok, false, false, s, pdl, &e))
+    choose<2, LS2, 2>(recurrence_kernel<TX, TG, LOGITS, 2, LS2, 2>, p, kTok, false, true, s, pdl, &e);
   return e;
 }
 
@@ -932,13 +934,13 @@ cudaError_t go(const RecurrenceGradLaunch &p, cudaStream_t s, bool pdl) {
   // As above, in tiles of 64 (16384 x 4096, 40 sequences, fp32: 209 us; 246 in tiles of 128, 269
   // with two channels a lane) or 32 (20000 x 256 in three sequences: 59 us, 92 in tiles of 64).
   cudaError_t e = cudaSuccess;
-  if (fits(4) && choose<4, 4, 2>(recurrence_grad_kernel<TX, TG, LOGITS, 4, 4, 2>, p, kTok, false, false, s, pdl, &e))
+  if (fits(4) &&
+      choose<4, 4, 2>(recurrence_grad_kernel<TX, TG, LOGITS, 4, 4, 2>, p, kTok, false, false, s, pdl, &e))
     return e;
-  if (!fits(2)) {
+  if (!fits(2))
     choose<1, 8, 1>(recurrence_grad_kernel<TX, TG, LOGITS, 1, 8, 1>, p, kTok, false, true, s, pdl, &e);
-  } else if (!choose<2, LS2, 1>(recurrence_grad_kernel<TX, TG, LOGITS, 2, LS2, 1>, p, kTok, false, false, s, pdl, &e)) {
+  else if (!choose<2, LS2, 1>(recurrence_grad_kernel<TX, TG, LOGITS, 2, LS2, 1>, p, kTok, false, false, s, pdl, &e))
     choose<2, LS2, 2>(recurrence_grad_kernel<TX, TG, LOGITS, 2, LS2, 2>, p, kTok, false, true, s, pdl, &e);
-  }
   return e;
 }
 
