@@ -849,8 +849,11 @@ Spread spread(const int32_t *cu, int n_seqs, int64_t T, int tiles, int chunk1) {
 template <int V, int G, typename Launch>
 cudaError_t launch_spread(void (*kern)(Launch, Parts), const Launch &p, const Spread &sp, int tiles, int stage,
                           cudaStream_t s, bool pdl) {
-  const size_t smem = (size_t)stages_of(stage) * stage + shared_bytes<V, G>(sp.S);
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  // The limit is the kernel's and the process's, not the call's: it is always set to the most that
+  // a launch of `kern` takes, so that another host thread's call never lowers it before this launch.
+  const size_t rings = (size_t)stages_of(stage) * stage, smem = rings + shared_bytes<V, G>(sp.S);
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             (int)(rings + shared_bytes<V, G>(kMaxCluster)));
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
