@@ -75,10 +75,12 @@ enum {
   TR_OUTPUT_GATE = 16u,      /* tr_replay_group(s): every layer's W_in carries H d_v more
                                 rows (z, after v) and the readout goes through the gated
                                 RMSNorm before the output projection (see below) */
-  TR_SCAN_STALL_TEST = 256u  /* tr_gdn_scan, test hook: the chunked chain kernel never
-                                announces its first state, so its bounded waits run out
-                                (after tr_set_wait_limit_ns) and the call ends with
-                                TR_ERR_TIMEOUT at tr_check; outputs undefined */
+  TR_SCAN_STALL_TEST = 256u  /* tr_gdn_scan, tr_linear_recurrence(_backward), test hook: the
+                                chunked chain kernel never announces its first state, or the
+                                last CTA of a recurrence's cluster never sends, so the
+                                bounded waits for it run out (after tr_set_wait_limit_ns) and
+                                the call ends with TR_ERR_TIMEOUT at tr_check; outputs
+                                undefined */
 };
 
 /* Human-readable message for the last failing call on this host thread. */
@@ -470,8 +472,8 @@ tr_status tr_projection_fp8(const uint8_t *a, int64_t a_stride, const float *a_s
  * No workspace; may be captured into a graph after one uncaptured call on the device (a replay
  * reads cu_seqlens again, but its spread over the GPU is the captured call's: keep the same
  * offsets).
- * The waits of a launch that spreads a sequence over a cluster are bounded (TR_ERR_TIMEOUT at
- * tr_check).  cu_seqlens that differ from cu_seqlens_host give an undefined result.
+ * The waits of a launch that spreads a sequence over a cluster are bounded (tr_set_wait_limit_ns;
+ * TR_ERR_TIMEOUT at tr_check).  cu_seqlens that differ from cu_seqlens_host give an undefined result.
  */
 enum { TR_GATE_LOGITS = 512u };  /* tr_linear_recurrence(_backward): the gate is a logit */
 
@@ -519,12 +521,14 @@ tr_status tr_linear_recurrence_backward(const tr_recurrence_grad_args *args, voi
 
 /*
  * tr_set_wait_limit_ns: the wall-clock limit of every bounded wait in the chunked scan's
- * kernels (their mbarrier waits on copies, products and the other roles of a CTA), for
- * calls made after it; 0 restores the default of 4 s, above 60 s is rejected.  A wait that
- * runs out makes its CTA stop: it lets the copies and products it already issued finish
- * (a drain bounded separately, at 0.2 s), writes no further output, and sets the device
- * error word that tr_check reports as TR_ERR_TIMEOUT; the outputs of that call are then
- * undefined, and later calls work normally.  Process-wide (not per thread or device).
+ * kernels (their mbarrier waits on copies, products and the other roles of a CTA) and in
+ * the gated linear recurrence's (those of a cluster's CTAs for each other), for calls made
+ * after it; 0 restores the default of 4 s, above 60 s is rejected.  A wait that runs out
+ * makes its CTA stop: it lets the copies and products it already issued finish (a drain
+ * bounded separately, at 0.2 s), writes no further output (a recurrence's goes on to the
+ * end of its tokens, without waiting again), and sets the device error word that tr_check
+ * reports as TR_ERR_TIMEOUT; the outputs of that call are then undefined, and later calls
+ * work normally.  Process-wide (not per thread or device).
  * Every legitimate wait ends within microseconds; a short limit serves to test this path.
  */
 tr_status tr_set_wait_limit_ns(uint64_t ns);

@@ -60,6 +60,13 @@ struct GemmFp8Launch {
 cudaError_t launch_gemm_fp8(const GemmFp8Launch &p, unsigned *err_word, cudaStream_t s, bool pdl,
                             std::string *err);
 
+// The bounded waits of a cluster's CTAs for each other.
+struct Waits {
+  unsigned *err_word;
+  unsigned long long limit_ns;
+  int hold_back;             // test: the last CTA of a cluster sends nothing
+};
+
 // h_t = a_t h_{t-1} + x_t per channel over packed sequences, a_t = exp(gate) or
 // exp(-softplus(gate)).
 struct RecurrenceLaunch {
@@ -72,7 +79,7 @@ struct RecurrenceLaunch {
   const float *h0;           // [N, C] or NULL
   void *y;                   // NULL: only the final states
   float *h_final;            // [N, C]
-  unsigned *err_word;
+  Waits waits;
 };
 cudaError_t launch_recurrence(const RecurrenceLaunch &p, cudaStream_t s, bool pdl);
 
@@ -88,7 +95,7 @@ struct RecurrenceGradLaunch {
   const float *h0, *dh_final;   // [N, C] or NULL
   void *dx, *dgate;
   float *dh0;                   // [N, C] or NULL
-  unsigned *err_word;
+  Waits waits;
 };
 cudaError_t launch_recurrence_grad(const RecurrenceGradLaunch &p, cudaStream_t s, bool pdl);
 

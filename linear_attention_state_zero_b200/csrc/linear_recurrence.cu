@@ -260,7 +260,8 @@ struct Shared {
   float A[SEGS][C], B[SEGS][C];    // (the value in front of a segment then takes its A's place)
   float start[SEGS];
   uint64_t bar[2];                 // every CTA's maps of a set are here
-  int abort;
+  int abort;                       // a wait ran out
+  int gave_up;                     // the last round that bar was armed for, then
   struct Cta {                     // (not allocated without a cluster)
     float A[C], B[C];
     float start;
@@ -274,23 +275,40 @@ size_t shared_bytes(int S) {
 
 // What a CTA starts with; with a cluster, every CTA's barriers are ready before any sends to it.
 template <int V, int G>
-__device__ __forceinline__ void begin(Shared<V, G> &sh, uint32_t S) {
+__device__ __forceinline__ void begin(Shared<V, G> &sh, uint32_t S, bool hold_back) {
   if (S == 1) return;
   if (threadIdx.x == 0) {
     mbar_init(smem_u32(&sh.bar[0]), 1);
     mbar_init(smem_u32(&sh.bar[1]), 1);
-    sh.abort = 0;
+    sh.abort = hold_back;   // (as if it had given up in front of the first round)
+    sh.gave_up = -1;
     fence_mbar_init();
   }
   __syncwarp();
   cluster_sync_all();
 }
 
-// After a wait that gave up, others may still be sending: no CTA of a cluster leaves before all.
-__device__ __forceinline__ void leave(uint32_t S) {
+// Arms the set of maps of round `round`: every CTA's bytes are to come.
+template <int V, int G>
+__device__ __forceinline__ uint32_t expect_maps(Shared<V, G> &sh, int round, uint32_t S) {
+  const uint32_t bar = smem_u32(&sh.bar[round & 1]);
+  mbar_arrive_expect_tx(bar, S * (8 * Shared<V, G>::C + 4));
+  return bar;
+}
+__device__ __forceinline__ uint32_t parity_of(int round) { return (uint32_t)(round >> 1) & 1u; }
+
+// No CTA of a cluster leaves before all have sent what they send.  One that gave up then lets arrive
+// what may be on its way to it: the maps of the round that it gave up in, and those of CTAs that got
+// through that round and sent the next one's (each wait bounded).
+template <int V, int G>
+__device__ __forceinline__ void leave(Shared<V, G> &sh, uint32_t S) {
   if (S == 1) return;
   __syncwarp();
   cluster_sync_all();
+  if (threadIdx.x != 0 || !sh.abort) return;
+  const int round = sh.gave_up;
+  if (round >= 0) mbar_wait_drain(smem_u32(&sh.bar[round & 1]), parity_of(round));
+  mbar_wait_drain(expect_maps(sh, round + 1, S), parity_of(round + 1));
 }
 
 // The sequence that holds token t0 (the last with cu <= t0: seq, its tokens from .. to - 1), and
@@ -349,9 +367,12 @@ __device__ __forceinline__ uint32_t lookup_down(const int32_t *__restrict__ cu, 
 // it.  The first 32 V / G threads own a channel each: they walk the segments' maps, and keep the
 // value in front of the round (`carry`) for the next.  (Every warp walking the maps before its
 // own for its own channels took a fifth of the kernel's instructions.)
+// A thread whose wait for the other CTAs gave up arms no barrier again, sends nothing (`sends`) and
+// waits no more: the rounds go on with undefined values to their end, where leave() meets the other
+// CTAs.  (Leaving the rounds took a test in each, 1-3% of a call's time.)
 template <int V, int G>
-__device__ __forceinline__ void join(Shared<V, G> &sh, int round, uint32_t S, uint32_t r, unsigned *err_word, int seg,
-                                     int li, const float (&A)[V], const float (&B)[V], bool start, float &carry,
+__device__ __forceinline__ void join(Shared<V, G> &sh, int round, uint32_t S, uint32_t r, uint32_t &sends,
+                                     const Waits &waits, int seg, int li, const float (&A)[V], const float (&B)[V], bool start, float &carry,
                                      float (&u)[V]) {
   typedef Shared<V, G> Sh;
   __syncwarp();
@@ -377,18 +398,21 @@ __device__ __forceinline__ void join(Shared<V, G> &sh, int round, uint32_t S, ui
       }
       const int par = round & 1;
       const uint32_t bar = smem_u32(&sh.bar[par]);
-      if (threadIdx.x == 0) mbar_arrive_expect_tx(bar, S * (8 * Sh::C + 4));
+      if (threadIdx.x == 0 && sends) expect_maps(sh, round, S);
       typename Sh::Cta &to = sh.cta[par][r];
       const uint32_t here = smem_u32(&to.A[ch]);
-      for (uint32_t k = 0; k < S; ++k) {
+      for (uint32_t k = 0; k < sends; ++k) {
         const uint32_t there = cluster_map(bar, k), dst = cluster_map(here, k);
         st_async(dst, ta, there);
         st_async(dst + 4 * Sh::C, tb, there);
         const float flag[1] = {ts ? 1.f : 0.f};
         if (threadIdx.x == 0) st_async(dst + 8 * Sh::C, flag, there);
       }
-      // (after a wait that gave up the rounds go on without waiting; the result is undefined)
-      mbar_wait(bar, (uint32_t)(round >> 1) & 1u, AbortFlag{&sh.abort, err_word, ERRBIT_SCAN_TIMEOUT});
+      const AbortFlag ab{&sh.abort, waits.err_word, ERRBIT_SCAN_TIMEOUT, waits.limit_ns};
+      if (sends && !mbar_wait(bar, parity_of(round), ab)) {
+        if (threadIdx.x == 0) sh.gave_up = round;
+        sends = 0;
+      }
       float mine = 0.f;
 #pragma unroll
       for (uint32_t k = 0; k < kMaxCluster; ++k) {
@@ -463,7 +487,8 @@ __global__ void __launch_bounds__(kW * 32, 2) recurrence_kernel(RecurrenceLaunch
   const int tb = parts.lo[blockIdx.y], te = parts.hi[blockIdx.y];
   const int chunk = (int)S * SEGS * LS;
   pdl_trigger();
-  begin(sh, S);
+  uint32_t sends = p.waits.hold_back && r + 1 == S ? 0 : S;   // CTAs that this thread sends its maps to
+  begin(sh, S, sends == 0);
   pdl_wait();
   // lanes past the last channel load the last ones and store nothing
   const int cl = live ? c : p.C - V;
@@ -552,7 +577,7 @@ __global__ void __launch_bounds__(kW * 32, 2) recurrence_kernel(RecurrenceLaunch
         vfma(B, a[i], B, x[i]);
         vmul(A, A, a[i]);
       }
-      join<V, G>(sh, round, S, r, p.err_word, seg, li, A, B, false, carry, u);
+      join<V, G>(sh, round, S, r, sends, p.waits, seg, li, A, B, false, carry, u);
 #pragma unroll
       for (int i = 0; i < LS; ++i) {
         vfma(u, a[i], u, x[i]);
@@ -582,7 +607,7 @@ __global__ void __launch_bounds__(kW * 32, 2) recurrence_kernel(RecurrenceLaunch
           if (mask >> (i + 1) & 1u) put_final(n, B);
         }
       }
-      join<V, G>(sh, round, S, r, p.err_word, seg, li, A, B, inside != 0, carry, u);
+      join<V, G>(sh, round, S, r, sends, p.waits, seg, li, A, B, inside != 0, carry, u);
 #pragma unroll
       for (int i = 0; i < LS; ++i) {
         if (i >= first) continue;
@@ -593,7 +618,7 @@ __global__ void __launch_bounds__(kW * 32, 2) recurrence_kernel(RecurrenceLaunch
     }
     stage = stage == STAGES - 1 ? 0 : stage + 1;
   }
-  leave(S);
+  leave(sh, S);
 }
 
 // Sequences of at most one token (decoding): h_final = a h0 + x, a thread per V channels.
@@ -645,7 +670,8 @@ __global__ void __launch_bounds__(kW * 32, 2) recurrence_grad_kernel(RecurrenceG
   const int tb = parts.lo[blockIdx.y], te = parts.hi[blockIdx.y];
   const int chunk = (int)S * SEGS * LS;
   pdl_trigger();
-  begin(sh, S);
+  uint32_t sends = p.waits.hold_back && r + 1 == S ? 0 : S;   // CTAs that this thread sends its maps to
+  begin(sh, S, sends == 0);
   pdl_wait();
   const int cl = live ? c : p.C - V;
   int t1 = te - 1 - ((int)r * SEGS + seg) * LS;
@@ -764,7 +790,7 @@ __global__ void __launch_bounds__(kW * 32, 2) recurrence_grad_kernel(RecurrenceG
         vmul(B, a[i], B);
         vmul(A, A, a[i]);
       }
-      join<V, G>(sh, round, S, r, p.err_word, seg, li, A, B, false, carry, u);
+      join<V, G>(sh, round, S, r, sends, p.waits, seg, li, A, B, false, carry, u);
 #pragma unroll
       for (int i = 0; i < LS; ++i) emit(i, u);
     } else {
@@ -786,7 +812,7 @@ __global__ void __launch_bounds__(kW * 32, 2) recurrence_grad_kernel(RecurrenceG
         emit(i, B);
         put_first(i, B);
       }
-      join<V, G>(sh, round, S, r, p.err_word, seg, li, A, B, ends != 0, carry, u);
+      join<V, G>(sh, round, S, r, sends, p.waits, seg, li, A, B, ends != 0, carry, u);
 #pragma unroll
       for (int i = 0; i < LS; ++i)
         if (i < first) {
@@ -796,7 +822,7 @@ __global__ void __launch_bounds__(kW * 32, 2) recurrence_grad_kernel(RecurrenceG
     }
     stage = stage == STAGES - 1 ? 0 : stage + 1;
   }
-  leave(S);
+  leave(sh, S);
 }
 
 // How a call is spread: runs of whole sequences (grid.y) times S CTAs of a cluster that share a

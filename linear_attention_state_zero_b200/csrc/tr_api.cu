@@ -1247,7 +1247,7 @@ tr_status check_recurrence(int32_t n_seqs, int32_t C, int64_t T, int32_t dtype, 
   if (T > 0x7fff0000LL || C > (1 << 24))
     return fail(TR_ERR_UNSUPPORTED, "total_tokens = %lld, n_channels = %d are too large", (long long)T, C);
   if (!known_dtype(dtype) || !known_dtype(gate_dtype)) return fail(TR_ERR_DTYPE, "dtype/gate_dtype");
-  if (flags & ~(unsigned)TR_GATE_LOGITS) return fail(TR_ERR_INVALID_ARG, "unknown recurrence flags 0x%x", flags);
+  if (flags & ~(unsigned)(TR_GATE_LOGITS | TR_SCAN_STALL_TEST)) return fail(TR_ERR_INVALID_ARG, "unknown recurrence flags 0x%x", flags);
   if (!cu) return fail(TR_ERR_INVALID_ARG, "cu_seqlens is NULL");
   if (!aligned4(cu)) return fail(TR_ERR_ALIGNMENT, "cu_seqlens must be 4-byte aligned");
   return check_cu_host(cu_host, n_seqs, T);
@@ -1296,7 +1296,9 @@ tr_status tr_linear_recurrence(const tr_recurrence_args *a, void *stream) {
   p.h_final = a->h_final;
   int dev;
   std::string err;
-  if (!device_state(static_cast<cudaStream_t>(stream), &dev, &p.err_word, &err)) return fail(TR_ERR_CUDA, "%s", err.c_str());
+  if (!device_state(static_cast<cudaStream_t>(stream), &dev, &p.waits.err_word, &err)) return fail(TR_ERR_CUDA, "%s", err.c_str());
+  p.waits.limit_ns = tr::scan_wait_limit_ns();
+  p.waits.hold_back = (a->flags & TR_SCAN_STALL_TEST) != 0;
   cudaError_t e = tr::launch_recurrence(p, static_cast<cudaStream_t>(stream), true);
   if (e != cudaSuccess) return cuda_fail(e, "linear recurrence");
   return ok();
@@ -1344,7 +1346,9 @@ tr_status tr_linear_recurrence_backward(const tr_recurrence_grad_args *a, void *
   p.dh0 = a->dh0;
   int dev;
   std::string err;
-  if (!device_state(static_cast<cudaStream_t>(stream), &dev, &p.err_word, &err)) return fail(TR_ERR_CUDA, "%s", err.c_str());
+  if (!device_state(static_cast<cudaStream_t>(stream), &dev, &p.waits.err_word, &err)) return fail(TR_ERR_CUDA, "%s", err.c_str());
+  p.waits.limit_ns = tr::scan_wait_limit_ns();
+  p.waits.hold_back = (a->flags & TR_SCAN_STALL_TEST) != 0;
   cudaError_t e = tr::launch_recurrence_grad(p, static_cast<cudaStream_t>(stream), true);
   if (e != cudaSuccess) return cuda_fail(e, "linear recurrence (backward)");
   return ok();

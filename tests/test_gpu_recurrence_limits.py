@@ -1,4 +1,5 @@
-"""The gated linear recurrence at the edges of its contract: calls from several host threads."""
+"""The gated linear recurrence at the edges of its contract: calls from several host threads,
+waits that run out."""
 import ctypes
 import threading
 
@@ -68,3 +69,39 @@ def test_host_threads_with_and_without_clusters(cuda_device, backward):
     assert refused == 0 and made == 1500 * len(calls)
     same = [torch.equal(a, b) for _, out, k, _, _ in calls for a, b in zip(out, want[k])]
     assert all(same)
+
+
+@pytest.mark.parametrize("limit_ns", [50_000_000, 1])
+@pytest.mark.parametrize("backward", [False, True])
+def test_waits_that_run_out(cuda_device, backward, limit_ns):
+    """The last CTA of each cluster sends nothing: the others give up at the limit, however short,
+    every CTA leaves, tr_check reports it, and the next calls are what they were."""
+    T, C = 4000, 2048
+    host, cu = tr.seqlens([0, T], cuda_device)
+    x, g = rnd((T, C), 1, BF).to(cuda_device), (rnd((T, C), 2) - 3).to(BF).to(cuda_device)
+    y, h = tr.linear_recurrence(x, g, (host, cu), gate_logits=True)
+    want = (y, h) + tr.linear_recurrence_backward(x, g, y, (host, cu), gate_logits=True)[:2]
+    out = [torch.empty_like(t) for t in want]
+    tr.check()
+    flags, stream = tr.TR_GATE_LOGITS | tr.TR_SCAN_STALL_TEST, torch.cuda.current_stream().cuda_stream
+    try:
+        tr.set_wait_limit_ns(limit_ns)
+        if backward:
+            a = tr.RecurrenceGradArgs(1, C, T, 1, 1, flags, 0, 0, 0, 0, 0, x.data_ptr(), g.data_ptr(), y.data_ptr(),
+                                      cu.data_ptr(), host.data_ptr(), None, None, out[2].data_ptr(),
+                                      out[3].data_ptr(), None)
+            assert tr.lib.tr_linear_recurrence_backward(ctypes.byref(a), stream) == 0
+        else:
+            a = tr.RecurrenceArgs(1, C, T, 1, 1, flags, 0, 0, 0, x.data_ptr(), g.data_ptr(), cu.data_ptr(),
+                                  host.data_ptr(), None, out[0].data_ptr(), out[1].data_ptr())
+            assert tr.lib.tr_linear_recurrence(ctypes.byref(a), stream) == 0
+        with pytest.raises(tr.TrError) as e:
+            tr.check()
+        assert e.value.status == 8   # TR_ERR_TIMEOUT
+    finally:
+        tr.set_wait_limit_ns(0)
+    tr.check()                       # the failed check cleared the error word
+    y, h = tr.linear_recurrence(x, g, (host, cu), gate_logits=True)
+    got = (y, h) + tr.linear_recurrence_backward(x, g, y, (host, cu), gate_logits=True)[:2]
+    tr.check()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
