@@ -464,7 +464,8 @@ tr_status tr_projection_fp8(const uint8_t *a, int64_t a_stride, const float *a_s
  * one token per sequence (decoding) is a call like any other: h_final may be h0, in place.
  *   x       [T, C] of dtype, gate [T, C] of gate_dtype (bf16 or fp32 each), token strides
  *           x_stride / gate_stride / y_stride elements (0 = C); any alignment of whole elements.
- *           Gates are not checked: exp(gate) > 1 grows, as written.
+ *           Gates are not checked: exp(gate) > 1 grows, as written (a_t is an fp32, infinite
+ *           for a gate above 88.7).
  *   cu_seqlens, cu_seqlens_host   as in tr_gdn_scan (empty sequences keep their state)
  *   h0      [N, C] fp32 or NULL
  *   y       [T, C] of dtype, or NULL to keep the final states only; not x or gate

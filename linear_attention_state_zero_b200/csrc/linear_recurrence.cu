@@ -145,20 +145,28 @@ __device__ __forceinline__ float rcp_ftz(float x) {
   return y;
 }
 
+__device__ __forceinline__ float min_nan(float a, float b) {   // (a NaN stays)
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 // a, good to 2^-21: ex2 and rcp (approximate, 2^-22 each) of a rounded argument.  (e^gate may be
 // infinite: a is 0 then.)  GRAD: also q = h d(log a) / d(gate), with d(log a) / d(gate) = 1, or
 // -(1 - a) = -a e^gate for a logit; above 80, e^gate is held at e^80 there (a < 2e-35), so that
 // the product stays finite, and the minimum keeps a NaN.
+// Without LOGITS, l += log2 a.
 template <bool LOGITS, bool GRAD, int V>
-__device__ __forceinline__ void decay(float (&g)[V], float (&a)[V], const float (&h)[V], float (&q)[V]) {
+__device__ __forceinline__ void decay(float (&g)[V], float (&a)[V], const float (&h)[V], float (&q)[V], float (&l)[V]) {
   float e[V], one[V], log2e[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     one[v] = 1.f;
     log2e[v] = 1.4426950408889634f;
-    if (LOGITS && GRAD) asm("min.NaN.f32 %0, %1, %2;" : "=f"(g[v]) : "f"(g[v]), "f"(80.f));
+    if (LOGITS && GRAD) g[v] = min_nan(g[v], 80.f);
   }
   vmul(e, g, log2e);
+  if (!LOGITS) vadd(l, l, e);
 #pragma unroll
   for (int v = 0; v < V; ++v) e[v] = ex2_ftz(e[v]);
   if (!LOGITS) {
@@ -180,10 +188,32 @@ __device__ __forceinline__ void decay(float (&g)[V], float (&a)[V], const float 
   }
 }
 template <bool LOGITS, int V>
-__device__ __forceinline__ void decay(float (&g)[V], float (&a)[V]) {
+__device__ __forceinline__ void decay(float (&g)[V], float (&a)[V], float (&l)[V]) {
   float none[V] = {};
-  decay<LOGITS, false>(g, a, none, none);
+  decay<LOGITS, false>(g, a, none, none, l);
 }
+
+// The decays of a map u -> A u + B.  exp(gate) may be above 1, and their product then leave fp32's
+// range, on the way or at its end, where the values that it is for do not: a zero in front would
+// become inf * 0, a tiny value infinite, one that shrinks and grows again 0.  So without LOGITS a map
+// keeps F = sqrt(A), from the sum of its decays' logarithms.  Its ends are those of A = 2^254, which
+// takes the least normal fp32 past the largest, and of 2^-252, which takes the largest below 2^-124.
+// With LOGITS (a <= 1) it keeps A itself.  (Backward 32768 x 2048: 237 us with products of such
+// decays too, 236 with F; 285 with A as a logarithm that the joining threads apply in three factors.)
+template <bool LOGITS>
+struct Decays {
+  // a segment's, from the product or the sum of log2 a
+  static __device__ __forceinline__ float of(float p) {
+    if (LOGITS) return p;
+    return ex2_ftz(min_nan(0.5f * p, 127.f));
+  }
+  static __device__ __forceinline__ float both(float a, float b) {
+    return LOGITS ? a * b : min_nan(a * b, 3.4028235e38f);
+  }
+  static __device__ __forceinline__ float apply(float A, float v, float B) {
+    return LOGITS ? fmaf(A, v, B) : fmaf(A * v, A, B);
+  }
+};
 
 // What a thread reads of one operand, V channels of LS tokens a round, a few rounds ahead: a ring
 // in shared memory that the thread alone fills and reads, by asynchronous copies, so that it
@@ -364,19 +394,23 @@ __device__ __forceinline__ uint32_t lookup_down(const int32_t *__restrict__ cu, 
 }
 
 // Joins the maps of a round.  In: the map of this lane's segment.  Out: the value in front of
-// it.  The first 32 V / G threads own a channel each: they walk the segments' maps, and keep the
+// it (A: the product of its decays, or without LOGITS the sum of their logarithms to base 2).  The
+// first 32 V / G threads own a channel each: they walk the segments' maps, and keep the
 // value in front of the round (`carry`) for the next.  (Every warp walking the maps before its
 // own for its own channels took a fifth of the kernel's instructions.)
 // A thread whose wait for the other CTAs gave up arms no barrier again, sends nothing (`sends`) and
 // waits no more: the rounds go on with undefined values to their end, where leave() meets the other
 // CTAs.  (Leaving the rounds took a test in each, 1-3% of a call's time.)
-template <int V, int G>
+template <bool LOGITS, int V, int G>
 __device__ __forceinline__ void join(Shared<V, G> &sh, int round, uint32_t S, uint32_t r, uint32_t &sends,
-                                     const Waits &waits, int seg, int li, const float (&A)[V], const float (&B)[V], bool start, float &carry,
-                                     float (&u)[V]) {
+                                     const Waits &waits, int seg, int li, const float (&A)[V], const float (&B)[V],
+                                     bool start, float &carry, float (&u)[V]) {
   typedef Shared<V, G> Sh;
   __syncwarp();
-  st_f32(&sh.A[seg][li * V], A);
+  float of[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) of[v] = Decays<LOGITS>::of(A[v]);
+  st_f32(&sh.A[seg][li * V], of);
   st_f32(&sh.B[seg][li * V], B);
   if (li == 0) sh.start[seg] = start ? 1.f : 0.f;
   const bool any = __syncthreads_or(start);
@@ -384,7 +418,7 @@ __device__ __forceinline__ void join(Shared<V, G> &sh, int round, uint32_t S, ui
     const int ch = threadIdx.x;
     // u after a segment: one that a sequence begins in forgets what came before
     auto after = [&](int w, float v) {
-      return any && sh.start[w] != 0.f ? sh.B[w][ch] : fmaf(sh.A[w][ch], v, sh.B[w][ch]);
+      return any && sh.start[w] != 0.f ? sh.B[w][ch] : Decays<LOGITS>::apply(sh.A[w][ch], v, sh.B[w][ch]);
     };
     float v = carry;
     if (S > 1) {
@@ -393,7 +427,7 @@ __device__ __forceinline__ void join(Shared<V, G> &sh, int round, uint32_t S, ui
 #pragma unroll
       for (int w = 0; w < Sh::SEGS; ++w) {
         tb[0] = after(w, tb[0]);
-        ta[0] *= sh.A[w][ch];
+        ta[0] = Decays<LOGITS>::both(ta[0], sh.A[w][ch]);
         ts = ts || (any && sh.start[w] != 0.f);
       }
       const int par = round & 1;
@@ -419,7 +453,7 @@ __device__ __forceinline__ void join(Shared<V, G> &sh, int round, uint32_t S, ui
         if (k >= S) break;
         const typename Sh::Cta &m = sh.cta[par][k];
         if (k == r) mine = v;
-        v = m.start != 0.f ? m.B[ch] : fmaf(m.A[ch], v, m.B[ch]);
+        v = m.start != 0.f ? m.B[ch] : Decays<LOGITS>::apply(m.A[ch], v, m.B[ch]);
       }
       carry = v;
       v = mine;
@@ -548,21 +582,20 @@ __global__ void __launch_bounds__(kW * 32, 2) recurrence_kernel(RecurrenceLaunch
     }
     fetch(stage == 0 ? STAGES - 1 : stage - 1);   // into the slots of the round before
     cp_wait<STAGES - 1>();
-    float a[LS][V], x[LS][V];
+    float a[LS][V], x[LS][V], A[V], B[V], u[V];
 #pragma unroll
-    for (int i = 0; i < LS; ++i) {
+    for (int v = 0; v < V; ++v) {
+      A[v] = LOGITS ? 1.f : 0.f;
+      B[v] = 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < LS; ++i) {   // (tokens that do not exist have gates 0)
       float g[V];
       to_f32(rg.get(stage, i), g);
       to_f32(rx.get(stage, i), x[i]);
-      decay<LOGITS>(g, a[i]);
+      decay<LOGITS>(g, a[i], A);
     }
     const bool whole = lim == LS && (mask & ~(1u << LS)) == 0;   // of one sequence, begun before
-    float A[V], B[V], u[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      A[v] = 1.f;
-      B[v] = 0.f;
-    }
     auto put = [&](int i, const float (&h)[V]) {
       if (put_y) st_f32(py + i * p.y_stride, h);
     };
@@ -575,9 +608,9 @@ __global__ void __launch_bounds__(kW * 32, 2) recurrence_kernel(RecurrenceLaunch
 #pragma unroll
       for (int i = 0; i < LS; ++i) {
         vfma(B, a[i], B, x[i]);
-        vmul(A, A, a[i]);
+        if (LOGITS) vmul(A, A, a[i]);
       }
-      join<V, G>(sh, round, S, r, sends, p.waits, seg, li, A, B, false, carry, u);
+      join<LOGITS>(sh, round, S, r, sends, p.waits, seg, li, A, B, false, carry, u);
 #pragma unroll
       for (int i = 0; i < LS; ++i) {
         vfma(u, a[i], u, x[i]);
@@ -600,14 +633,14 @@ __global__ void __launch_bounds__(kW * 32, 2) recurrence_kernel(RecurrenceLaunch
           for (int v = 0; v < V; ++v) B[v] = p.h0 ? fmaf(a[i][v], hb[v], x[i][v]) : x[i][v];
         } else {
           vfma(B, a[i], B, x[i]);
-          vmul(A, A, a[i]);
+          if (LOGITS) vmul(A, A, a[i]);
         }
         if (i >= first) {
           put(i, B);
           if (mask >> (i + 1) & 1u) put_final(n, B);
         }
       }
-      join<V, G>(sh, round, S, r, sends, p.waits, seg, li, A, B, inside != 0, carry, u);
+      join<LOGITS>(sh, round, S, r, sends, p.waits, seg, li, A, B, inside != 0, carry, u);
 #pragma unroll
       for (int i = 0; i < LS; ++i) {
         if (i >= first) continue;
@@ -640,7 +673,8 @@ __global__ void __launch_bounds__(256) recurrence_step_kernel(RecurrenceLaunch p
       float x[V], g[V];
       to_f32(ld_raw<TX, V>(reinterpret_cast<const TX *>(p.x) + t * p.x_stride + c), x);
       to_f32(ld_raw<TG, V>(reinterpret_cast<const TG *>(p.gate) + t * p.gate_stride + c), g);
-      decay<LOGITS>(g, g);
+      float none[V] = {};
+      decay<LOGITS>(g, g, none);
 #pragma unroll
       for (int v = 0; v < V; ++v) h[v] = p.h0 ? fmaf(g[v], h[v], x[v]) : x[v];
       if (p.y) st_f32(reinterpret_cast<TX *>(p.y) + t * p.y_stride + c, h);
@@ -746,6 +780,12 @@ __global__ void __launch_bounds__(kW * 32, 2) recurrence_grad_kernel(RecurrenceG
     if (e1 >= 0 && p.dh_final) state(p.dh_final, e1, he);
     fetch(stage == 0 ? STAGES - 1 : stage - 1);   // into the slots of the round before
     cp_wait<STAGES - 1>();
+    float A[V], B[V], u[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      A[v] = LOGITS ? 1.f : 0.f;
+      B[v] = 0.f;
+    }
     float a[LS][V], d[LS][V], q[LS][V];   // q = h_{t-1} d(log a)/d(gate)
 #pragma unroll
     for (int i = 0; i < LS; ++i) {
@@ -758,13 +798,7 @@ __global__ void __launch_bounds__(kW * 32, 2) recurrence_grad_kernel(RecurrenceG
 #pragma unroll
         for (int v = 0; v < V; ++v) h[v] = hb[v];
       }
-      decay<LOGITS, true>(g, a[i], h, q[i]);
-    }
-    float A[V], B[V], u[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      A[v] = 1.f;
-      B[v] = 0.f;
+      decay<LOGITS, true>(g, a[i], h, q[i], A);
     }
     // the token's gradients; on entry u is what reaches h_t from behind, on exit u_t
     auto emit = [&](int i, float (&uu)[V]) {
@@ -788,9 +822,9 @@ __global__ void __launch_bounds__(kW * 32, 2) recurrence_grad_kernel(RecurrenceG
       for (int i = 0; i < LS; ++i) {
         vadd(B, d[i], B);
         vmul(B, a[i], B);
-        vmul(A, A, a[i]);
+        if (LOGITS) vmul(A, A, a[i]);
       }
-      join<V, G>(sh, round, S, r, sends, p.waits, seg, li, A, B, false, carry, u);
+      join<LOGITS>(sh, round, S, r, sends, p.waits, seg, li, A, B, false, carry, u);
 #pragma unroll
       for (int i = 0; i < LS; ++i) emit(i, u);
     } else {
@@ -801,7 +835,7 @@ __global__ void __launch_bounds__(kW * 32, 2) recurrence_grad_kernel(RecurrenceG
         if (i < first) {
           vadd(B, d[i], B);
           vmul(B, a[i], B);
-          vmul(A, A, a[i]);
+          if (LOGITS) vmul(A, A, a[i]);
           continue;
         }
         if (ends >> i & 1u) {
@@ -812,7 +846,7 @@ __global__ void __launch_bounds__(kW * 32, 2) recurrence_grad_kernel(RecurrenceG
         emit(i, B);
         put_first(i, B);
       }
-      join<V, G>(sh, round, S, r, sends, p.waits, seg, li, A, B, ends != 0, carry, u);
+      join<LOGITS>(sh, round, S, r, sends, p.waits, seg, li, A, B, ends != 0, carry, u);
 #pragma unroll
       for (int i = 0; i < LS; ++i)
         if (i < first) {
