@@ -151,10 +151,11 @@ __device__ __forceinline__ float min_nan(float a, float b) {   // (a NaN stays)
   return r;
 }
 
-// a, good to 2^-21: ex2 and rcp (approximate, 2^-22 each) of a rounded argument.  (e^gate may be
-// infinite: a is 0 then.)  GRAD: also q = h d(log a) / d(gate), with d(log a) / d(gate) = 1, or
-// -(1 - a) = -a e^gate for a logit; above 80, e^gate is held at e^80 there (a < 2e-35), so that
-// the product stays finite, and the minimum keeps a NaN.
+// a by ex2 and rcp (approximate, 2^-22 each) of a rounded argument: off by at most 2^-22 + 2^-23 |gate|
+// of itself (2^-21 + 2^-23 |gate| for a logit; measured next to a = 1: 1.4 x 2^-24, as expf).  e^gate
+// may be infinite: a is 0 then, as where it is below 2^-126.  GRAD: also q = h d(log a) / d(gate),
+// with d(log a) / d(gate) = 1, or -(1 - a) = -a e^gate for a logit, e^gate held finite there (a is 0
+// before it is not, and so is the product).
 // Without LOGITS, l += log2 a.
 template <bool LOGITS, bool GRAD, int V>
 __device__ __forceinline__ void decay(float (&g)[V], float (&a)[V], const float (&h)[V], float (&q)[V], float (&l)[V]) {
@@ -163,7 +164,6 @@ __device__ __forceinline__ void decay(float (&g)[V], float (&a)[V], const float 
   for (int v = 0; v < V; ++v) {
     one[v] = 1.f;
     log2e[v] = 1.4426950408889634f;
-    if (LOGITS && GRAD) g[v] = min_nan(g[v], 80.f);
   }
   vmul(e, g, log2e);
   if (!LOGITS) vadd(l, l, e);
@@ -181,6 +181,8 @@ __device__ __forceinline__ void decay(float (&g)[V], float (&a)[V], const float 
 #pragma unroll
   for (int v = 0; v < V; ++v) a[v] = rcp_ftz(a[v]);
   if (GRAD) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) e[v] = min_nan(e[v], 3.4028235e38f);
     vmul(e, e, a);
 #pragma unroll
     for (int v = 0; v < V; ++v) e[v] = -e[v];

@@ -226,3 +226,25 @@ def test_growing_gates_and_waits_that_run_out(cuda_device, backward):
     got = call()
     tr.check()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("gd", [BF, F32])
+def test_gradients_of_gates_that_forget_everything(cuda_device, gd):
+    """Gate logits up to where the decay leaves fp32's range, under gradients that make it visible:
+    dh0 and dgate take the decay that the forward pass takes, and 0 where that is 0."""
+    N, C = 30, 64
+    g = torch.linspace(60, 87, N * C).reshape(N, C).to(gd)
+    g[-1] = torch.tensor([90.0, 300.0, 1e30, float("inf")]).repeat(C // 4).to(gd)
+    dy, h0 = 1e30 * (1 + rnd((N, C), 1).abs()), rnd((N, C), 2)
+    cu = list(range(N + 1))
+    dev = [t.to(cuda_device) for t in (dy, g, h0)]
+    y, a = tr.linear_recurrence(torch.zeros_like(dev[0]), dev[1], cu, h0=torch.ones_like(dev[0]), gate_logits=True)
+    dx, dg, dh0 = tr.linear_recurrence_backward(dev[0], dev[1], y, cu, h0=dev[2], gate_logits=True)
+    # one product each from the forward pass's decays; 1 - a is 1, and e^gate a has their error twice
+    assert torch.equal(dx, dev[0])
+    assert (np.abs(f64(dh0) - f64(a) * f64(dy)) <= 2.0 ** -24 * np.abs(f64(dh0))).all()
+    want = -f64(dh0) * f64(h0)
+    assert (np.abs(f64(dg) - want) <= (2.0 ** -20 + HALF[gd]) * np.abs(want)).all()
+    assert (f64(a)[-1] == 0).all() and (f64(dh0)[-1] == 0).all() and (f64(dg)[-1] == 0).all()
+    ref_a = 1 / (1 + np.exp(f64(g)[:-1]))
+    assert (np.abs(f64(a)[:-1] - ref_a) <= (2.0 ** -21 + 87 * 2.0 ** -23) * ref_a).all()
