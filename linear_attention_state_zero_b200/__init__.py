@@ -591,16 +591,23 @@ _FP8 = torch.float8_e4m3fn
 _DTYPES = {torch.float32: TR_DTYPE_F32, torch.bfloat16: TR_DTYPE_BF16}
 
 
+def _handle_of_current_stream(index):
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+def _empty_strided(shape, strides, dtype):
+    return torch.empty_strided(shape, strides, dtype=dtype, device="cuda")
+
+
 # What a call of a small operator costs is the host's: 4 us to make a Stream object, 1.7 us for
-# each output that torch.empty allocates, 0.8 us by the allocator's direct entry (where this
-# build of torch has it), 2.5 us for the launch.
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_device_index = torch._C._cuda_getDevice
+# each output that torch.empty allocates, 0.8 us by the allocator's direct entry, 2.5 us for the
+# launch.  A build of torch that lacks a direct entry (one without CUDA has none) takes the public one.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _handle_of_current_stream)
+_device_index = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 try:
     from torch._C._dynamo.guards import _empty_strided_cuda
 except ImportError:
-    def _empty_strided_cuda(shape, strides, dtype):
-        return torch.empty_strided(shape, strides, dtype=dtype, device="cuda")
+    _empty_strided_cuda = _empty_strided
 
 
 def _matrix_of(rows, cols, dtype):
