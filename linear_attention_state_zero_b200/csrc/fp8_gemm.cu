@@ -343,7 +343,7 @@ __global__ void __launch_bounds__(PairCfg<BN>::THREADS, 1)
 #pragma unroll
         for (int j = 0; j < NC / 16; ++j) {
           float v[16];
-          tmem_ld<16>(tbase + (uint32_t)(b * BN + 16 * j), v);
+          tmem_ld(tbase + (uint32_t)(b * BN + 16 * j), v);
           tc_wait_ld();
           if (j + 1 == NC / 16) {
             tc_fence_before();
@@ -598,7 +598,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
 #pragma unroll
         for (int j = 0; j < NT; j += 16) {
           float v[16];
-          tmem_ld<16>(tbase + (uint32_t)(buf * NT + j), v);
+          tmem_ld(tbase + (uint32_t)(buf * NT + j), v);
           tc_wait_ld();
 #pragma unroll
           for (int i = 0; i < 16; ++i) acc[j + i] = fmaf(v[i], sc[at * NT + j + i], acc[j + i]);

@@ -75,27 +75,15 @@ __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap
       : "memory");
 }
 
-// 32 lanes x NC consecutive fp32 columns: thread i of the warp gets lane (base + i).  The loads
+// 32 lanes x 16 consecutive fp32 columns: thread i of the warp gets lane (base + i).  The loads
 // write float registers: through integer ones, as in tr_ptx.cuh, every value is copied once
 // more, which doubles the instructions of a loop that uses each value once.
-template <int NC> __device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&v)[NC]);
-template <> __device__ __forceinline__ void tmem_ld<16>(uint32_t taddr, float (&v)[16]) {
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&v)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {"
       "%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
       : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
         "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
-      : "r"(taddr));
-}
-template <> __device__ __forceinline__ void tmem_ld<32>(uint32_t taddr, float (&v)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
-      "%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
-        "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]),
-        "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]),
-        "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
       : "r"(taddr));
 }
 
@@ -129,25 +117,13 @@ __device__ __forceinline__ uint32_t cluster_map(uint32_t local, uint32_t rank) {
 __device__ __forceinline__ void st_cluster(uint32_t cluster_addr, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_addr), "f"(v) : "memory");
 }
-// V floats to another CTA's shared memory, counted there as 4 V bytes of `bar`'s transaction
+// A float to another CTA's shared memory, counted there as 4 bytes of `bar`'s transaction
 // (shared::cluster addresses of one CTA).  Nothing else of this thread is waited for, as a
 // cluster barrier's release does with every global access in flight.
-__device__ __forceinline__ void st_async(uint32_t dst, const float (&f)[1], uint32_t bar) {
+__device__ __forceinline__ void st_async(uint32_t dst, float f, uint32_t bar) {
   asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(dst),
-               "r"(__float_as_uint(f[0])), "r"(bar)
+               "r"(__float_as_uint(f)), "r"(bar)
                : "memory");
-}
-__device__ __forceinline__ void st_async(uint32_t dst, const float (&f)[2], uint32_t bar) {
-  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.b32 [%0], {%1, %2}, [%3];" ::"r"(dst),
-               "r"(__float_as_uint(f[0])), "r"(__float_as_uint(f[1])), "r"(bar)
-               : "memory");
-}
-__device__ __forceinline__ void st_async(uint32_t dst, const float (&f)[4], uint32_t bar) {
-  asm volatile(
-      "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(dst),
-      "r"(__float_as_uint(f[0])), "r"(__float_as_uint(f[1])), "r"(__float_as_uint(f[2])),
-      "r"(__float_as_uint(f[3])), "r"(bar)
-      : "memory");
 }
 // Arrive on an mbarrier of any CTA of the cluster (a shared::cluster address) without ordering
 // other memory accesses: what the waiter reuses is tensor memory whose loads have completed

@@ -424,12 +424,12 @@ __device__ __forceinline__ void join(Shared<V, G> &sh, int round, uint32_t S, ui
     };
     float v = carry;
     if (S > 1) {
-      float ta[1] = {1.f}, tb[1] = {0.f};
+      float ta = 1.f, tb = 0.f;
       bool ts = false;
 #pragma unroll
       for (int w = 0; w < Sh::SEGS; ++w) {
-        tb[0] = after(w, tb[0]);
-        ta[0] = Decays<LOGITS>::both(ta[0], sh.A[w][ch]);
+        tb = after(w, tb);
+        ta = Decays<LOGITS>::both(ta, sh.A[w][ch]);
         ts = ts || (any && sh.start[w] != 0.f);
       }
       const int par = round & 1;
@@ -441,8 +441,7 @@ __device__ __forceinline__ void join(Shared<V, G> &sh, int round, uint32_t S, ui
         const uint32_t there = cluster_map(bar, k), dst = cluster_map(here, k);
         st_async(dst, ta, there);
         st_async(dst + 4 * Sh::C, tb, there);
-        const float flag[1] = {ts ? 1.f : 0.f};
-        if (threadIdx.x == 0) st_async(dst + 8 * Sh::C, flag, there);
+        if (threadIdx.x == 0) st_async(dst + 8 * Sh::C, ts ? 1.f : 0.f, there);
       }
       const AbortFlag ab{&sh.abort, waits.err_word, ERRBIT_SCAN_TIMEOUT, waits.limit_ns};
       if (sends && !mbar_wait(bar, parity_of(round), ab)) {
