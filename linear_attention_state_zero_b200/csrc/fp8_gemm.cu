@@ -344,7 +344,7 @@ __global__ void __launch_bounds__(PairCfg<BN>::THREADS, 1)
         for (int j = 0; j < NC / 16; ++j) {
           float v[16];
           tmem_ld(tbase + (uint32_t)(b * BN + 16 * j), v);
-          tc_wait_ld();
+          tc_wait_ld(v);
           if (j + 1 == NC / 16) {
             tc_fence_before();
             __syncwarp();
@@ -599,7 +599,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         for (int j = 0; j < NT; j += 16) {
           float v[16];
           tmem_ld(tbase + (uint32_t)(buf * NT + j), v);
-          tc_wait_ld();
+          tc_wait_ld(v);
 #pragma unroll
           for (int i = 0; i < 16; ++i) acc[j + i] = fmaf(v[i], sc[at * NT + j + i], acc[j + i]);
         }

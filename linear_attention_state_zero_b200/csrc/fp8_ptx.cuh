@@ -87,6 +87,15 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&v)[16]) {
       : "r"(taddr));
 }
 
+// Waits for this warp's loads from tensor memory.  What they wrote counts as written here: the
+// compiler may otherwise move uses of the values, which it takes for the loads' results, in front
+// of the wait.
+__device__ __forceinline__ void tc_wait_ld(float (&v)[16]) {
+  tc_wait_ld();
+#pragma unroll
+  for (int i = 0; i < 16; ++i) asm volatile("" : "+f"(v[i]));
+}
+
 // ------------------------------------------------------------------ clusters
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
