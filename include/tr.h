@@ -429,7 +429,8 @@ tr_status tr_out_projection(const void *o, int64_t o_stride, const void *W_o, co
  *   gain [D] fp32 or NULL (ones); eps 0 -> 1e-6
  *   q [n_rows, D] e4m3, scale [n_rows, ceil(D / 128)] fp32, packed
  *   res_out   [n_rows, D] of res_dtype, or NULL; may be the residual itself (same stride)
- * D a multiple of 16, at most 32768; rows 16-byte aligned.
+ * D a multiple of 16, at most 32768; rows and gain 16-byte aligned.  The squares are summed in
+ * fp32: a row whose sum of squares passes 3e38 normalises to 0.
  */
 tr_status tr_rmsnorm_fp8(const void *x, int32_t x_dtype, int64_t x_stride, const void *residual,
                          int32_t res_dtype, int64_t res_stride, const float *gain, int64_t n_rows,
@@ -460,6 +461,7 @@ tr_status tr_projection_fp8(const uint8_t *a, int64_t a_stride, const float *a_s
  *   h_t = a_t h_{t-1} + x_t,  y_t = h_t,  h_final = h at each sequence's last token
  *   a_t = exp(gate_t), or with TR_GATE_LOGITS a_t = exp(-softplus(gate_t)) = 1 / (1 + e^gate_t)
  * from h0 (NULL: zero start, as in a tail replay).  States and sums are fp32; y is rounded once.
+ * a_t is off by at most (2^-21 + 2^-23 |gate_t|) a_t; next to 1 by 1.4 x 2^-24.
  * The result is bitwise reproducible, and no value of one sequence reaches another.  A batch of
  * one token per sequence (decoding) is a call like any other: h_final may be h0, in place.
  *   x       [T, C] of dtype, gate [T, C] of gate_dtype (bf16 or fp32 each), token strides
@@ -468,7 +470,8 @@ tr_status tr_projection_fp8(const uint8_t *a, int64_t a_stride, const float *a_s
  *           for a gate above 88.7).
  *   cu_seqlens, cu_seqlens_host   as in tr_gdn_scan (empty sequences keep their state)
  *   h0      [N, C] fp32 or NULL
- *   y       [T, C] of dtype, or NULL to keep the final states only; not x or gate
+ *   y       [T, C] of dtype, or NULL to keep the final states only; not x or gate, and not on
+ *           any of their elements
  *   h_final [N, C] fp32
  * No workspace; may be captured into a graph after one uncaptured call on the device (a replay
  * reads cu_seqlens again, but its spread over the GPU is the captured call's: keep the same
@@ -502,7 +505,7 @@ tr_status tr_linear_recurrence(const tr_recurrence_args *args, void *stream);
  * front of dgate's own), and from h0 (NULL: 0) at a sequence's first token.
  *   dy, y, dx [T, C] of dtype; gate, dgate [T, C] of gate_dtype; strides as above
  *   h0, dh_final [N, C] fp32 or NULL;  dh0 [N, C] fp32 or NULL (may be dh_final, in place)
- * dx and dgate must not be dy, gate, y or each other.
+ * dx and dgate must not be dy, gate, y or each other, nor share elements with them.
  */
 typedef struct tr_recurrence_grad_args {
   int32_t n_seqs, n_channels;

@@ -754,7 +754,8 @@ def linear_recurrence(x, gate, cu_seqlens, *, h0=None, gate_logits=False, want_y
                       h_final=None, stream=None):
     """h_t = a_t h_{t-1} + x_t per channel over packed sequences: (y [T, C] or None, h_final
     [N, C] fp32).  a = exp(gate), or exp(-softplus(gate)) with gate_logits.  h0 [N, C] fp32
-    (None: zero start); h_final may be h0.  For a captured call give cu_seqlens as seqlens()."""
+    (None: zero start); h_final may be h0.  For a captured call give cu_seqlens as seqlens().
+    The outputs carry no autograd history; linear_recurrence_backward gives the gradients."""
     T, C = _matrix("x", x)
     dev = _need_cuda(x, gate, h0, y, h_final)
     if stream is not None or _device_index() != dev.index:

@@ -130,7 +130,7 @@ constexpr int kNV = 4;   // 8-element vectors a lane holds of its row
 // lane v % 32 of warp (v / 32) % WPR, so 16 neighbouring lanes hold a scale block and each
 // warp's accesses are contiguous.  A few vectors per lane and several warps per row, rather than a warp per
 // row with the whole row in its registers, so that a few rows use many warps too.
-// A vector's division is done by one lane in four, as in quantize_rows_kernel.
+// A vector's division is done by one lane in NV, as in quantize_rows_kernel (one in four there).
 template <bool XBF, bool RES, bool RBF, int WPR, int NV>
 __global__ void __launch_bounds__(WPR < 8 ? 256 : WPR * 32)
     rmsnorm_fp8_kernel(NormFp8Launch p) {

@@ -19,10 +19,13 @@
 // reproducible.
 //
 // HBM bounds it where the runs of sequences fill the GPU: 65536 x 4096 bf16 in 64 sequences takes
-// 255 us (96% of the measured copy rate), backward 16384 x 4096 fp32 in 40 sequences 209 us (98%).
-// One long sequence is bound by the join of its cluster each round (backward 32768 x 2048, bf16
-// with fp32 gates: 230 us, 62%), a few thousand tokens by the latency of a few rounds of about
-// 2 us, and rows that are not 4-byte (bf16) or 8-byte (fp32) aligned by one channel a lane (35-70%).
+// 252 us with exponential gates and 264-270 with logits (98% and 91-93% of the measured copy rate;
+// up to 307 us on another GPU), backward 453 and 480 (90% and 85%: segments of 4 tokens, a join
+// for every 64), backward 16384 x 4096 fp32 in 40 sequences 213 us (96%).  One long sequence is
+// bound by the join of its cluster each round (65536 x 1024 bf16: 153-163 us, 40%; backward
+// 32768 x 2048, bf16 with fp32 gates: 235 us, 61%), a few thousand tokens by the latency of a few
+// rounds of about 2 us, and rows that are not 4-byte (bf16) or 8-byte (fp32) aligned by one channel
+// a lane (35-70%).
 //
 // The packed tokens are scanned as one long sequence that starts over where a sequence
 // begins.  That is a selection, not a product with a = 0, so infinities or NaN of one
@@ -219,7 +222,8 @@ struct Decays {
 
 // What a thread reads of one operand, V channels of LS tokens a round, a few rounds ahead: a ring
 // in shared memory that the thread alone fills and reads, by asynchronous copies, so that it
-// waits for nothing but its own copies, and the data in flight take no registers.
+// waits for nothing but its own copies, and the data in flight take no registers (but for one
+// channel of two bytes, see there).
 template <typename T, int V, int LS>
 struct Slots {
   static constexpr int TOKEN = kW * 32 * V * (int)sizeof(T);   // of a CTA
@@ -256,7 +260,7 @@ struct Ring : Slots<T, V, LS> {
   }
 };
 // Two bytes are too few for an asynchronous copy: the loads of a stage wait in registers until
-// the next stage is issued.
+// the next stage is issued, so that one stage is in flight at a time whatever the ring holds.
 template <int LS>
 struct Ring<__nv_bfloat16, 1, LS> : Slots<__nv_bfloat16, 1, LS> {
   Raw<__nv_bfloat16, 1> next[LS];
