@@ -1,4 +1,5 @@
-"""What the 8-bit steps make of infinities and NaN, over whole blocks and rows."""
+"""What the 8-bit steps make of the smallest blocks, and of infinities and NaN over whole blocks and
+rows."""
 import numpy as np
 import pytest
 import torch
@@ -45,3 +46,15 @@ def test_norm_of_a_row_that_is_not_finite(cuda_device, D, bad):
     rest = np.r_[v[3, :128], v[3, 256:]]
     assert np.isnan(rest).all() if np.isnan(bad) else (rest == 0).all()
     assert np.array_equal(f64(out), f64(x), equal_nan=True)
+
+
+def test_smallest_blocks(cuda_device):
+    """Largest magnitudes around 448 x 2^-126, where the scale stays at 2^-126, and below."""
+    x = torch.randn(40, 256, generator=torch.Generator().manual_seed(2)).clamp(-3, 3)
+    x = (x / 3 * 448 * 2.0 ** -126 * torch.logspace(-3, 1, 40, base=2)[:, None]).to(BF)
+    q, s = tr.quantize_fp8(x.to(cuda_device))
+    v = f64(x)
+    full = ref.expand_scales(ref.block_scales(v, 1), 1, *v.shape)
+    assert (np.abs(f64(s) - ref.block_scales(v, 1)) <= 2.0 ** -24 * f64(s)).all() and f64(s).min() == 2.0 ** -126
+    # half a step of q, next to which the scale, its reciprocal and the product are off by 2^-24 each
+    assert (np.abs(f64(q) * full - v) <= np.maximum(np.abs(v) * 2.0 ** -4, full * 2.0 ** -10) * (1 + 2.0 ** -22)).all()
